@@ -32,7 +32,8 @@ extern "C" {
 
 typedef enum {
   RMT_OK = 0,
-  RMT_EINVAL = 1,    /* bad argument: null pointer, unsupported shape, size out of range */
+  RMT_EINVAL = 1,    /* bad argument: null pointer, unsupported shape, size out of range (rmt_sync: a
+                      * length or page table entry on the device that does not fit its cache) */
   RMT_ENOMEM = 2,    /* device or pinned allocation failed */
   RMT_ECUDA = 3,     /* a CUDA runtime call or launch failed */
   RMT_ETIMEOUT = 4,  /* a bounded device-side wait gave up (reported by rmt_sync) */
@@ -365,6 +366,89 @@ rmt_status rmt_memory_write_noalloc(const float* y, const void* w_mkv, float* A,
  * x [rows, d] fp32, g [d] and y [rows, d] in dtype. d % 4 == 0. */
 rmt_status rmt_rmsnorm(const float* x, const void* g, void* y, int32_t rows, int32_t d, float eps,
                        rmt_dtype dtype, void* stream);
+
+/* ------------------------------------------------------------------------------------
+ * Attention over a window, and a 4-bit key/value cache for it: the streaming counterpart of
+ * the recurrent memory. A prompt runs through rmt_attention_window and its keys and values go
+ * into the cache (rmt_cache_write); from then on each token is one rmt_cache_write and one
+ * rmt_attention_cache per layer. Everywhere here row i of a sequence sees the keys
+ *   j <= i with i - j < window or j < sinks        (window = 0: every j <= i).
+ * Device pointers only; the call runs on the device that holds qkv (or pages), whatever the
+ * current device is, and `stream` must belong to that device. No call allocates device memory,
+ * so each may be captured into a CUDA graph; run each operator once on a device before capturing
+ * it there (modules are loaded at the first call). Nothing is kept between calls. A length or page table entry that does
+ * not fit the cache is found on the device: the rows concerned are skipped, and
+ * rmt_sync(NULL, stream) reports RMT_EINVAL.
+ * ------------------------------------------------------------------------------------ */
+
+/* rmt_attention over a window with sinks, for prompts of different lengths:
+ *   out[g, i, h] = softmax_j(q[g,i,h] . k[g,j,h/(H/Hkv)] / sqrt(dh)) v[g,j,h/(H/Hkv)], j as above.
+ * qkv [G, M, (H + 2*Hkv)*dh] (q heads, then k heads, then v heads), out [G, M, H*dh]; dh in
+ * {32, 64, 128}; dtype RMT_F32 or RMT_BF16. lens: device int32 [G], the rows each sequence has
+ * (clamped to 0 .. M), or NULL (M each); rows behind a sequence's last are not read as keys or
+ * values, and their out rows are left as they were. What a row does not see cannot reach it,
+ * even if it is not finite; a row that sees a value that is not finite gets an out row of that
+ * head that is not finite (which of inf and NaN, and in which channels, is not specified).
+ * Pointers 16-byte aligned; G, H <= 65535, M <= 2^30. */
+rmt_status rmt_attention_window(const void* qkv, void* out, int32_t G, int32_t M, int32_t H, int32_t Hkv,
+                                int32_t dh, int32_t window, int32_t sinks, const int32_t* lens, rmt_dtype dtype,
+                                void* stream);
+
+/* A key/value cache of one layer in 4 bits, in pages of RMT_CACHE_PAGE tokens. All pointers are
+ * the caller's device memory.
+ *   pages       n_pages * rmt_cache_page_bytes(n_kv_heads, head_dim) bytes, 16-byte aligned. Needs
+ *               no initial value.
+ *   page_table  int32 [n_seqs, max_pages]: token t of sequence b is row t % 64 of page
+ *               page_table[b][t / 64]. Entries past a sequence's last page are not read.
+ *   lens        int32 [n_seqs]: tokens of each sequence, those of the current call included;
+ *               0 for an unused slot of a padded batch.
+ * Sequences may share pages that none of them writes any more. A page holds, per kv head, one
+ * block of 72*head_dim bytes: key codes [64][head_dim/2], key scales [64][head_dim/16], value
+ * codes, value scales. 16 consecutive channels x share a scale byte: the f16 with bits byte << 7
+ * nearest to max|x| / 7 (ties to even; at most 9216); a channel's 4 bits (even channels in the
+ * low half of a byte) are q + 8, q = x / scale rounded to nearest (ties to even) within -7 .. 7,
+ * and stand for q * scale. 4.5 bits per channel. Magnitudes above 64512 saturate, infinities
+ * among them; a NaN is stored as 0; a block whose magnitudes are all at most 7 * 2^-18 is stored as 0. */
+#define RMT_CACHE_PAGE 64
+typedef struct {
+  void* pages;
+  const int32_t* page_table;
+  const int32_t* lens;
+  int32_t n_pages, n_seqs, max_pages, n_kv_heads, head_dim; /* head_dim 32, 64 or 128 */
+} rmt_cache;
+
+/* Bytes of one page; 0 for an unsupported shape. Needs no GPU. */
+size_t rmt_cache_page_bytes(int32_t n_kv_heads, int32_t head_dim);
+
+/* Quantise the newest rows of each sequence into the cache. k and v: row i of sequence b starts
+ * at element (b*M + i)*ld and holds n_kv_heads*head_dim values, so both may point into packed qkv
+ * rows (ld = (H + 2*Hkv)*dh). n_new: device int32 [n_seqs], the rows of each sequence (clamped to
+ * at most M), or NULL (M each). Row i < n_new[b] becomes token lens[b] - n_new[b] + i; rows whose
+ * token would be negative (an unused slot) are skipped. No two rows of one call may fall on the
+ * same token of a page. dtype RMT_F32 or RMT_BF16; k, v and the bytes of ld multiples of 16. */
+rmt_status rmt_cache_write(const rmt_cache* c, const void* k, const void* v, int64_t ld, int32_t M,
+                           const int32_t* n_new, rmt_dtype dtype, void* stream);
+
+/* The inverse: the values the cache holds for the same rows (exact in either dtype). Rows of k
+ * and v that are not among a sequence's newest n_new[b] are left as they were. */
+rmt_status rmt_cache_read(const rmt_cache* c, void* k, void* v, int64_t ld, int32_t M, const int32_t* n_new,
+                          rmt_dtype dtype, void* stream);
+
+/* Bytes of workspace that rmt_attention_cache needs for these sizes (lens and the tables are not
+ * read); 0, with a message, for sizes it refuses. Needs no GPU. */
+size_t rmt_attention_cache_workspace(const rmt_cache* c, int32_t n_q, int32_t H, int32_t window, int32_t sinks);
+
+/* Attention of the newest n_q tokens of each sequence (1 .. 64; positions lens[b] - n_q ..
+ * lens[b] - 1, each seeing what it may of the cache, the newest tokens included, so write them
+ * first) over the pages. q: row i of sequence b starts at element (b*n_q + i)*ldq and holds H*head_dim
+ * values; out [n_seqs, n_q, H*head_dim]; both in dtype (RMT_F32 or RMT_BF16). Keys and values are
+ * the ones rmt_cache_read gives; softmax and sums in fp32. A row that sees no key (a
+ * negative position) gives zeros. The workspace needs no initial value and may be used again by
+ * later calls on the same stream; calls that may overlap (two streams, two graphs replayed at
+ * once) need one each. Equal calls give equal bits. */
+rmt_status rmt_attention_cache(const rmt_cache* c, const void* q, int64_t ldq, void* out, int32_t n_q, int32_t H,
+                               int32_t window, int32_t sinks, void* workspace, size_t workspace_bytes,
+                               rmt_dtype dtype, void* stream);
 
 #ifdef __cplusplus
 }

@@ -155,14 +155,25 @@ struct DeviceScratch {
 };
 DeviceScratch g_dev_scratch[64];
 
+// Error word of the kernel-level entry points on the current device: a variable of the library's
+// module (zero when loaded), so a first call needs no allocation.
+__device__ int g_err_word;
+
+rmt_status current_error_word(int** err) {
+  void* p = nullptr;
+  RMT_CUDA(cudaGetSymbolAddress(&p, g_err_word));
+  *err = static_cast<int*>(p);
+  return RMT_OK;
+}
+
 rmt_status device_scratch(int G, const Cell** cells, int** err) {
   int dev = 0;
   RMT_CUDA(cudaGetDevice(&dev));
   if (dev < 0 || dev >= 64) return fail(RMT_EINVAL, "device index out of range");
   DeviceScratch& s = g_dev_scratch[dev];
   if (!s.err) {
-    RMT_CUDA(cudaMalloc(&s.err, sizeof(int)));
-    RMT_CUDA(cudaMemset(s.err, 0, sizeof(int)));
+    const rmt_status st = current_error_word(&s.err);
+    if (st != RMT_OK) return st;
   }
   if (G > s.cap) {
     const int cap = G > 4096 ? G : 4096;
@@ -208,6 +219,7 @@ rmt_status partial_scratch(size_t floats, float** out) {
 namespace rmt {
 // Lets other translation units of the library report through rmt_last_error().
 void set_last_error(const std::string& msg) { g_last_error = msg; }
+rmt_status device_error_word(int** err) { return current_error_word(err); }
 }  // namespace rmt
 
 struct rmt_handle {
@@ -1472,6 +1484,10 @@ rmt_status rmt_sync(rmt_handle* h, void* stream) {
     if (word & kErrBounds)
       return fail(RMT_EDEBUG, "a kernel's bounds check failed: a cell index fell outside its buffers (error word " +
                                   std::to_string(word) + ")");
+    if (word == kErrPage)
+      return fail(RMT_EINVAL,
+                  "a cache operator met a length or a page table entry outside its cache; the rows concerned were "
+                  "neither read nor written");
     if (word == kErrF16Range)
       return fail(RMT_ERANGE,
                   "a value of magnitude 65520 or more was stored as an f16 tensor-core operand (bf16 mode): the "

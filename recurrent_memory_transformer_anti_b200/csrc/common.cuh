@@ -19,6 +19,7 @@ enum : int {
   kErrTimeoutSelftest = 16,  // the bounded-wait check (rmt_wait_selftest) gave up, as it should
   kErrF16Range = 32,         // a value stored as an f16 tensor-core operand overflowed (see below)
   kErrBounds = 64,           // debug build: a cell's index fell outside the buffers it addresses
+  kErrPage = 128,            // a cache operator met a length or a page table entry outside its cache
 };
 
 // f16 operand range. In bf16 mode the tensor-core operands the forward writes (the residual

@@ -35,7 +35,8 @@ EXPORTED = ("rmt_create", "rmt_reserve", "rmt_forward", "rmt_forward_resume", "r
             "rmt_bounds_selftest",
             "rmt_destroy", "rmt_last_error", "rmt_grouped_gemm_bf16", "rmt_attention", "rmt_memory_read",
             "rmt_memory_update", "rmt_memory_update_sequential", "rmt_memory_write", "rmt_memory_write_noalloc", "rmt_rmsnorm", "rmt_probe",
-            "rmt_probe_read")
+            "rmt_probe_read", "rmt_attention_window", "rmt_cache_page_bytes", "rmt_cache_write", "rmt_cache_read",
+            "rmt_attention_cache_workspace", "rmt_attention_cache")
 
 KERNELS = ("assemble", "memq", "memread", "memo", "rmsnorm1", "qkv", "attention", "o", "rmsnorm2", "gateup", "down",
            "memkv", "memupdate", "emit")
@@ -52,6 +53,15 @@ class rmt_cfg(ctypes.Structure):
                                                "seg_len", "n_mem", "d_k", "d_v")] + \
                [("rope_theta", ctypes.c_float), ("rms_eps", ctypes.c_float), ("mem_eps", ctypes.c_float),
                 ("dtype", ctypes.c_int), ("mem_update", ctypes.c_int)]
+
+
+RMT_CACHE_PAGE = 64  # tokens per page of the 4-bit key/value cache
+
+
+class rmt_cache_struct(ctypes.Structure):
+    """struct rmt_cache of include/rmt.h."""
+    _fields_ = [("pages", ctypes.c_void_p), ("page_table", ctypes.c_void_p), ("lens", ctypes.c_void_p)] + \
+               [(n, ctypes.c_int32) for n in ("n_pages", "n_seqs", "max_pages", "n_kv_heads", "head_dim")]
 
 
 _PP = ctypes.POINTER(ctypes.c_void_p)
@@ -96,10 +106,19 @@ def _load() -> ctypes.CDLL:
                            ctypes.POINTER(ctypes.c_double), ctypes.POINTER(ctypes.c_double),
                            ctypes.POINTER(ctypes.c_int64)],
     }
+    cache = ctypes.POINTER(rmt_cache_struct)
+    sigs.update({
+        "rmt_attention_window": [vp, vp, i32, i32, i32, i32, i32, i32, i32, vp, ctypes.c_int, vp],
+        "rmt_cache_page_bytes": [i32, i32],
+        "rmt_cache_write": [cache, vp, vp, ctypes.c_int64, i32, vp, ctypes.c_int, vp],
+        "rmt_cache_read": [cache, vp, vp, ctypes.c_int64, i32, vp, ctypes.c_int, vp],
+        "rmt_attention_cache_workspace": [cache, i32, i32, i32, i32],
+        "rmt_attention_cache": [cache, vp, ctypes.c_int64, vp, i32, i32, i32, i32, vp, sz, ctypes.c_int, vp],
+    })
     for name, args in sigs.items():
         fn = getattr(lib, name)
         fn.argtypes = args
-        fn.restype = ctypes.c_int
+        fn.restype = sz if name in ("rmt_cache_page_bytes", "rmt_attention_cache_workspace") else ctypes.c_int
     lib.rmt_last_error.argtypes = []
     lib.rmt_last_error.restype = ctypes.c_char_p
     return lib
@@ -136,6 +155,30 @@ def _ptr(x):
             raise ValueError("tensors must be contiguous")
         return x.data_ptr()
     raise TypeError(f"cannot take the address of {type(x)}")
+
+
+def _ptr32(x):
+    """Raw address of an int32 array (None -> NULL)."""
+    if x is not None and not isinstance(x, int) and "int32" not in str(x.dtype):
+        raise TypeError(f"an int32 array is needed, not {x.dtype}")
+    return _ptr(x)
+
+
+def _rows(x, n: int, M: int, width: int, dtype: str):
+    """Address and row stride (elements) of n * M rows of `width` values: a tensor [n, M, ...] whose rows
+    are contiguous and equally spaced, possibly a slice of wider rows."""
+    if dtype not in ("f32", "bf16") or ("bfloat16" if dtype == "bf16" else "float32") not in str(x.dtype):
+        raise TypeError(f"rows of type {x.dtype} given as {dtype!r}")
+    shape, st = tuple(x.shape), x.stride()
+    if x.ndim < 3 or shape[:2] != (n, M) or x.numel() != n * M * width:
+        raise ValueError(f"rows must be [{n}, {M}, {width}], not {shape}")
+    ld = st[1] if M > 1 else st[0] if n > 1 else width
+    inner = [1]
+    for s in reversed(shape[3:]):
+        inner.insert(0, inner[0] * s)
+    if ld < width or (n > 1 and st[0] != M * ld) or any(a != b for a, b, s in zip(st[2:], inner, shape[2:]) if s > 1):
+        raise ValueError("rows must be contiguous and equally spaced")
+    return x.data_ptr(), ld
 
 
 def _stream(stream):
@@ -323,6 +366,75 @@ def rmt_memory_write_noalloc(y, w_mkv, A, z, G, n, d, dk, dv, eps, dtype="f32", 
 
 def rmt_rmsnorm(x, g, y, rows, d, eps, dtype="f32", stream=None) -> None:
     _check(_lib.rmt_rmsnorm(_ptr(x), _ptr(g), _ptr(y), rows, d, eps, DTYPES[dtype], _stream(stream)), "rmt_rmsnorm")
+
+
+def rmt_attention_window(qkv, out, G, M, H, Hkv, dh, window, sinks=0, lens=None, dtype="bf16", stream=None) -> None:
+    """Attention over a sliding window (0: none) and the first `sinks` tokens; lens: int32 [G] on the device or None."""
+    _check(_lib.rmt_attention_window(_ptr(qkv), _ptr(out), G, M, H, Hkv, dh, window, sinks, _ptr32(lens),
+                                     DTYPES[dtype], _stream(stream)), "rmt_attention_window")
+
+
+class Cache:
+    """An rmt_cache (include/rmt.h) together with the tensors it points to."""
+
+    def __init__(self, struct: rmt_cache_struct, keep: tuple):
+        self.struct = struct
+        self.keep = keep
+
+
+def rmt_cache_page_bytes(n_kv_heads: int, head_dim: int) -> int:
+    n = _lib.rmt_cache_page_bytes(n_kv_heads, head_dim)
+    if n == 0:
+        raise ValueError(f"no cache page for {n_kv_heads} heads of {head_dim}")
+    return n
+
+
+def rmt_cache(pages, page_table, lens, n_kv_heads: int, head_dim: int) -> Cache:
+    """The 4-bit key/value cache in these device tensors: pages (uint8, whole pages), page_table (int32
+    [n_seqs, max_pages]) and lens (int32 [n_seqs]). Their contents may change between calls."""
+    size = pages.numel() * pages.element_size()
+    page = rmt_cache_page_bytes(n_kv_heads, head_dim)
+    if size % page or page_table.ndim != 2 or lens.ndim != 1 or lens.shape[0] != page_table.shape[0]:
+        raise ValueError(f"pages must hold whole pages of {page} bytes, page_table [n_seqs, max_pages] and lens [n_seqs]")
+    s = rmt_cache_struct(_ptr(pages), _ptr32(page_table), _ptr32(lens), size // page, page_table.shape[0],
+                         page_table.shape[1], n_kv_heads, head_dim)
+    return Cache(s, (pages, page_table, lens))
+
+
+def rmt_cache_write(cache: Cache, k, v, M, n_new=None, dtype="bf16", stream=None) -> None:
+    """Quantise rows k, v ([n_seqs, M, n_kv_heads * head_dim], views into wider rows allowed) into the cache."""
+    width = cache.struct.n_kv_heads * cache.struct.head_dim
+    (pk, ld), (pv, ldv) = (_rows(x, cache.struct.n_seqs, M, width, dtype) for x in (k, v))
+    if ld != ldv:
+        raise ValueError("k and v need the same row stride")
+    _check(_lib.rmt_cache_write(ctypes.byref(cache.struct), pk, pv, ld, M, _ptr32(n_new), DTYPES[dtype],
+                                _stream(stream)), "rmt_cache_write")
+
+
+def rmt_cache_read(cache: Cache, k, v, M, n_new=None, dtype="bf16", stream=None) -> None:
+    """The values the cache holds for the rows rmt_cache_write takes, into k, v."""
+    width = cache.struct.n_kv_heads * cache.struct.head_dim
+    (pk, ld), (pv, ldv) = (_rows(x, cache.struct.n_seqs, M, width, dtype) for x in (k, v))
+    if ld != ldv:
+        raise ValueError("k and v need the same row stride")
+    _check(_lib.rmt_cache_read(ctypes.byref(cache.struct), pk, pv, ld, M, _ptr32(n_new), DTYPES[dtype],
+                               _stream(stream)), "rmt_cache_read")
+
+
+def rmt_attention_cache_workspace(cache: Cache, n_q: int, H: int, window: int = 0, sinks: int = 0) -> int:
+    n = _lib.rmt_attention_cache_workspace(ctypes.byref(cache.struct), n_q, H, window, sinks)
+    if n == 0:
+        raise RmtError(RMT_EINVAL, "rmt_attention_cache_workspace", rmt_last_error())
+    return n
+
+
+def rmt_attention_cache(cache: Cache, q, out, n_q, H, window, sinks, workspace, dtype="bf16", stream=None) -> None:
+    """Attention of the newest n_q tokens of each sequence (q rows [n_seqs, n_q, H * head_dim], a view into
+    wider rows allowed) over the cache. workspace: a uint8 tensor of rmt_attention_cache_workspace bytes."""
+    pq, ldq = _rows(q, cache.struct.n_seqs, n_q, H * cache.struct.head_dim, dtype)
+    _check(_lib.rmt_attention_cache(ctypes.byref(cache.struct), pq, ldq, _ptr(out), n_q, H, window, sinks,
+                                    _ptr(workspace), workspace.numel() * workspace.element_size(), DTYPES[dtype],
+                                    _stream(stream)), "rmt_attention_cache")
 
 
 def storage(a, dtype: str, device=None):
