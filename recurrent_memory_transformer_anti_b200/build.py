@@ -22,7 +22,7 @@ LIB = os.path.join(PKG, "librmt.so")
 OBJDIR_DEBUG = os.path.join(PKG, "_build_debug")
 LIB_DEBUG = os.path.join(PKG, "librmt_debug.so")
 SOURCES = ["api.cu", "tc_gemm.cu", "tc_gemm_pair.cu", "simt_gemm.cu", "attention.cu", "attention_tc.cu", "memory.cu", "memory_tc.cu", "rowops.cu", "noalloc.cu",
-           "selftest.cu", "attention_window.cu", "attention_cache.cu", "cache4.cu", "cache_api.cu"]
+           "selftest.cu", "attention_window.cu", "attention_window_tc.cu", "attention_cache.cu", "cache4.cu", "cache_api.cu"]
 
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo", "-std=c++17",

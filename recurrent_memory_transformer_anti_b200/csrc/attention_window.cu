@@ -7,7 +7,8 @@
 // channels of the output in registers; a row's maximum and sum run along (one pass over the keys).
 // Key rows past the sequence's end are never read. A weight of zero adds nothing even when the
 // value it belongs to is not finite, so what is masked cannot reach a row.
-// Bound by the fp32 FMA pipe and the shared-memory reads that feed it.
+// Bound by the fp32 FMA pipe and the shared-memory reads that feed it. Serves fp32, and bf16 heads
+// of 32 (bf16 heads of 64 and 128: attention_window_tc.cu).
 #include "cache4.cuh"
 #include "launch.h"
 
@@ -200,10 +201,11 @@ cudaError_t launch_simt(const WindowAttnArgs& a, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_window_attention(const WindowAttnArgs& a, int dh, bool bf16, cudaStream_t st) {
+  if (bf16 && dh >= 64) return launch_window_attention_tc(a, dh, st);
   switch (dh) {
     case 32: return bf16 ? launch_simt<32, __nv_bfloat16>(a, st) : launch_simt<32, float>(a, st);
-    case 64: return bf16 ? launch_simt<64, __nv_bfloat16>(a, st) : launch_simt<64, float>(a, st);
-    case 128: return bf16 ? launch_simt<128, __nv_bfloat16>(a, st) : launch_simt<128, float>(a, st);
+    case 64: return launch_simt<64, float>(a, st);
+    case 128: return launch_simt<128, float>(a, st);
   }
   return cudaErrorInvalidValue;
 }

@@ -122,5 +122,6 @@ struct WindowAttnArgs {
   int* err;
 };
 cudaError_t launch_window_attention(const WindowAttnArgs& a, int dh, bool bf16, cudaStream_t st);
+cudaError_t launch_window_attention_tc(const WindowAttnArgs& a, int dh, cudaStream_t st);  // bf16, dh 64 or 128
 
 }  // namespace rmt
