@@ -1,91 +1,698 @@
 // Attention of a sequence's newest tokens over its pages of the 4-bit key/value cache.
+//
+// One pass over the codes, which is what bounds it: 72 dh bytes per 64 tokens and kv head. The
+// work of a call is a list of units -- 64 tokens of one kv head (32 at head_dim 128: 4608 bytes
+// either way) for one tile of query rows -- sorted by sequence, head, tile and position, leaving out what no
+// row sees between the sinks and the window. Each CTA takes an equal, contiguous share of the list whatever the
+// lengths are (they are read on the device), so one long sequence and many short ones are both
+// spread over all SMs. A CTA's eight warps take the units of an (item, CTA) stretch in turn; each
+// has its own ring of bulk copies and its own running maximum, sum and output, which are added at the
+// end of the stretch. A stretch that is a whole item gives its result; the others go to the
+// workspace, and a second kernel adds them in the order of the keys: no atomics, equal bits.
+//
+// Arithmetic. Query rows are the MMA's N (8 or 16 rows: the heads of a group, times the tokens),
+// keys or channels its M, so that few rows waste nothing: S^T = K Q^T, O^T = V^T P^T
+// (mma.sync m16n8k16, f16 operands, fp32 sums: the codes turn into operands in registers, and tcgen05
+// would have them pass through shared memory again, four times their bytes). A code's nibble
+// or-ed into the f16 pattern of 64 is 64 + (q + 8); times the scale minus 72 scales is q * scale,
+// exact, in one fused operation for two codes. Scales are taken at 2^-4 of their value so that 72 of
+// them stay in f16's range; the factor comes back with the row's scale and at the end. A lane takes 16
+// (or 8, or 32) consecutive channels of a key, since the order of a dot product's terms is free as long as
+// Q has the same one, and for V eight neighbouring lanes' keys are chosen so that the reads of a warp are
+// whole lines of shared memory. P^T turns from accumulator to operand layout by
+// movmatrix. Queries are scaled by a power of two per row into f16's normal range: exact for
+// bf16; fp32 queries and weights are taken as two f16 terms (22 bits). Weights are held at 2^15 of
+// their value (at most 32768): what f16 cuts off is below 2^-40 of the largest.
 #include "cache4.cuh"
 #include "launch.h"
+#include "sm100.cuh"
 
 namespace rmt {
 namespace {
 
+using cache4::CacheArgs;
 using cache4::kPage;
 
-// One CTA per (query row, query head): 64 threads, one key each, then the channels.
-template <int DH, typename T>
-__global__ void __launch_bounds__(64) cache_attn_simple_kernel(const CacheAttnArgs a) {
-  using L = cache4::Layout<DH>;
-  __shared__ float qs[DH], p[kPage], red[2];
-  const int h = blockIdx.x, qi = blockIdx.y, b = blockIdx.z, t = threadIdx.x;
-  const int head = h / (a.H / a.c.Hkv);
-  const int len = a.c.lens[b], pos = len - a.n_q + qi;
-  const T* q = static_cast<const T*>(a.q) + (static_cast<size_t>(b) * a.n_q + qi) * a.ldq + h * DH;
-  bool odd = false;  // a query that is not finite
-  for (int i = t; i < DH; i += 64) {
-    qs[i] = to_f32(q[i]) * rsqrtf(static_cast<float>(DH));
-    odd |= !isfinite(qs[i]);
-  }
-  odd = __syncthreads_or(odd);
-  float o[DH / 32], m = -INFINITY, l = 0.f;
-  for (int i = 0; i < DH / 32; ++i) o[i] = 0.f;
-  int top = pos;
-  if (pos >= a.c.max_pages * kPage) {  // a length past the cache
-    if (t == 0 && a.c.err) atomicOr(a.c.err, kErrPage);
-    top = -1;
-  }
-  for (int k0 = 0; k0 <= top; k0 += kPage) {
-    if (k0 + kPage <= pos - a.window + 1 && k0 >= a.sinks) continue;
-    const int page = cache4::page_of(a.c, b, k0);
-    if (page < 0) continue;
-    const unsigned char* blk = a.c.pages + cache4::block_offset<DH>(a.c, page, head);
-    const int key = k0 + t;
-    float s = -INFINITY;
-    if (key <= top && (pos - key < a.window || key < a.sinks)) {
-      s = 0.f;
-      for (int i = 0; i < DH; ++i) {
-        const int code = (blk[t * L::CODE_ROW + i / 2] >> (4 * (i & 1))) & 15;
-        s += qs[i] * static_cast<float>(code - 8) * cache4::decode_scale(blk[L::CODES + t * L::SCALE_ROW + i / 16]);
-      }
-    }
-    float mx = s;
-    for (int w = 16; w; w >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
-    __syncthreads();
-    if ((t & 31) == 0) red[t >> 5] = mx;
-    __syncthreads();
-    mx = fmaxf(m, fmaxf(red[0], red[1]));
-    if (mx == -INFINITY) continue;
-    p[t] = s == -INFINITY ? 0.f : expf(s - mx);
-    const float corr = m == -INFINITY ? 0.f : expf(m - mx);
-    m = mx;
-    __syncthreads();
-    l *= corr;
-    for (int i = 0; i < DH / 32; ++i) o[i] *= corr;
-    for (int r = 0; r < kPage; ++r) {
-      if (p[r] == 0.f) continue;
-      l += p[r];
-      for (int i = 0; i * 64 + t < DH; ++i) {
-        const int c = i * 64 + t;
-        const int code = (blk[L::V_OFF + r * L::CODE_ROW + c / 2] >> (4 * (c & 1))) & 15;
-        o[i] += p[r] * static_cast<float>(code - 8) *
-                cache4::decode_scale(blk[L::V_OFF + L::CODES + r * L::SCALE_ROW + c / 16]);
-      }
-    }
-  }
-  T* out = static_cast<T*>(a.out) + ((static_cast<size_t>(b) * a.n_q + qi) * a.H + h) * DH;
-  for (int i = 0; i * 64 + t < DH; ++i) out[i * 64 + t] = from_f32<T>(odd && pos >= 0 ? NAN : l > 0.f ? o[i] / l : 0.f);
+constexpr int kWarps = 8, kStages = 2;
+constexpr int kMaxCtas = 296;  // two per SM
+constexpr float kCodeScale = 16.f;  // operands hold 2^-4 of a value
+
+template <int DH>
+struct Unit {
+  static constexpr int TOK = DH == 128 ? 32 : 64;
+  static constexpr int CODES = TOK * DH / 2, SCALES = TOK * DH / 16;
+  static constexpr int V_OFF = CODES + SCALES;
+  static constexpr int BYTES = 2 * V_OFF;
+};
+
+// What of a sequence some row of it sees, in units: the first `sinks` of them, then from `lo` on.
+struct Span {
+  int n, sinks, lo;
+};
+struct SpanArgs {
+  const int* lens;
+  int cap;  // tokens a sequence may hold
+  int n_q, window, sinks;
+};
+template <int TOK>
+__device__ __forceinline__ Span span_of(const SpanArgs& a, int b) {
+  const int T = __ldg(a.lens + b);
+  Span s{0, 0, 0};
+  if (T <= 0 || T > a.cap) return s;
+  s.lo = max(0, max(T - a.n_q, 0) - a.window + 1) / TOK;
+  const int last = (T - 1) / TOK;
+  s.sinks = min((min(a.sinks, T) + TOK - 1) / TOK, s.lo);
+  s.n = s.sinks + last - s.lo + 1;
+  return s;
 }
 
-template <int DH, typename T>
-cudaError_t launch_simple(const CacheAttnArgs& a, cudaStream_t st) {
-  cache_attn_simple_kernel<DH, T><<<dim3(a.H, a.n_q, a.c.n_seqs), 64, 0, st>>>(a);
-  return cudaGetLastError();
+struct DecodeArgs {
+  CacheArgs c;
+  SpanArgs span;
+  const void* q;
+  long long ldq;
+  void* out;
+  int n_q, H, group, rows, tiles;  // rows: n_q * group per kv head, in `tiles` tiles
+  int* prefix;    // [n_seqs + 1] units before each sequence (workspace; for the second kernel)
+  float* parts;   // [2 * CTAs] stretches: O [dh][rows of a tile], maxima, sums
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t h2(__half2 v) { return *reinterpret_cast<uint32_t*>(&v); }
+__device__ __forceinline__ __half2 as_h2(uint32_t v) { return *reinterpret_cast<__half2*>(&v); }
+__device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                    uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+
+// Two scale bytes (low and high half of b) as f16 pairs: 2^-4 of the scales, and -72 times that.
+__device__ __forceinline__ void scale_pair(uint32_t b, __half2& s, __half2& c) {
+  s = __hmul2(as_h2(b << 7), __float2half2_rn(1.f / kCodeScale));
+  c = __hmul2(s, __float2half2_rn(-72.f));
+}
+// The codes j of the low and of the high half of w, j = 0..3, times their scales.
+__device__ __forceinline__ void dequant(uint32_t w, __half2 s, __half2 c, uint32_t (&v)[4]) {
+  const uint32_t m = 0x00F000F0u, one = 0x54005400u;
+  v[0] = h2(__hfma2(as_h2(((w << 4) & m) | one), s, c));
+  v[1] = h2(__hfma2(as_h2((w & m) | one), s, c));
+  v[2] = h2(__hfma2(as_h2(((w >> 4) & m) | one), s, c));
+  v[3] = h2(__hfma2(as_h2(((w >> 8) & m) | one), s, c));
+}
+
+template <int N>
+__device__ __forceinline__ void lds_words(const unsigned char* p, uint32_t (&w)[N]) {
+  if constexpr (N == 1) {
+    w[0] = *reinterpret_cast<const uint32_t*>(p);
+  } else if constexpr (N == 2) {
+    const uint2 u = *reinterpret_cast<const uint2*>(p);
+    w[0] = u.x, w[1] = u.y;
+  } else {
+    const uint4 u = *reinterpret_cast<const uint4*>(p);
+    w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
+  }
+}
+
+// Stretch of the unit list inside one (sequence, kv head, row tile).
+struct Stretch {
+  int b, head, tile;
+  int begin, end;  // the item's units
+  Span s;
+};
+
+template <int DH, int NT>
+struct DecodeSmem {
+  static constexpr int RING = 0;
+  static constexpr int LD = DH + 4;
+  static constexpr int MERGE = RING + kWarps * kStages * Unit<DH>::BYTES;  // [warp][8][LD] fp32
+  static constexpr int ML = MERGE + kWarps * 8 * LD * 4;                   // [2][warp][8 NT] fp32
+  static constexpr int PRE = ML + 2 * kWarps * 8 * NT * 4;                 // [257] units before each chunk of sequences
+  static constexpr int BAR = PRE + 272 * 4;
+  static constexpr int BYTES = BAR + kWarps * kStages * 8 + 16;
+};
+
+template <int DH, typename T, int NT, int MINB>
+__global__ void __launch_bounds__(32 * kWarps, MINB) cache_attn_kernel(const DecodeArgs a) {
+  using U = Unit<DH>;
+  using S = DecodeSmem<DH, NT>;
+  constexpr bool SPLIT = std::is_same_v<T, float>;  // two f16 terms per query and weight
+  constexpr int TERMS = SPLIT ? 2 : 1;
+  constexpr int KS = DH / 16, WK = DH / 32;  // k16 steps of a key, 32-bit words of it per lane
+  constexpr int MT = U::TOK / 16;            // 16-key tiles of a unit
+  constexpr int MU = DH / 16;                // 16-channel tiles
+  extern __shared__ __align__(128) unsigned char smem[];
+  float* const merge = reinterpret_cast<float*>(smem + S::MERGE);
+  float* const ml = reinterpret_cast<float*>(smem + S::ML);
+  int* const pre = reinterpret_cast<int*>(smem + S::PRE);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + S::BAR + kWarps * kStages * 8);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  unsigned char* const ring = smem + S::RING + warp * kStages * U::BYTES;
+  const uint32_t ring_s = sm100::smem_u32(ring);
+  const uint32_t bars = sm100::smem_u32(smem + S::BAR) + warp * kStages * 8;
+
+  pdl_trigger();
+  if (lane == 0)
+    for (int i = 0; i < kStages; ++i) sm100::mbar_init(bars + 8 * i, 1);
+  if (threadIdx.x == 0) *abort_flag = 0;
+  sm100::fence_barrier_init();
+  pdl_wait();  // lengths, table, pages and q come from earlier kernels of the stream
+
+  // units before each sequence: every thread counts a run of sequences, then a scan over the threads
+  const int n = a.c.n_seqs, run = (n + 32 * kWarps - 1) / (32 * kWarps);
+  const int per_seq = a.c.Hkv * a.tiles;
+  int units;
+  {
+    int mine = 0;
+    const int b0 = min(n, static_cast<int>(threadIdx.x) * run), b1 = min(n, b0 + run);
+    for (int b = b0; b < b1; ++b) {
+      mine += span_of<U::TOK>(a.span, b).n * per_seq;
+      if (blockIdx.x == 0 && a.c.err && __ldg(a.c.lens + b) > a.span.cap) atomicOr(a.c.err, kErrPage);
+    }
+    int sum = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += v;
+    }
+    if (lane == 31) pre[260 + warp] = sum;
+    __syncthreads();
+    int before = 0;
+    for (int w = 0; w < warp; ++w) before += pre[260 + w];
+    pre[threadIdx.x] = before + sum - mine;
+    if (threadIdx.x == 32 * kWarps - 1) pre[256] = before + sum;
+    if (blockIdx.x == 0) {
+      int at = before + sum - mine;
+      for (int b = b0; b < b1; ++b) {
+        a.prefix[b] = at;
+        at += span_of<U::TOK>(a.span, b).n * per_seq;
+      }
+      if (threadIdx.x == 32 * kWarps - 1) a.prefix[n] = before + sum;
+    }
+    __syncthreads();
+    units = pre[256];
+  }
+  // this CTA's share: at least a unit per warp, the CTAs past that have none
+  const int ctas = min(static_cast<int>(gridDim.x), (units + kWarps - 1) / kWarps);
+  if (static_cast<int>(blockIdx.x) >= ctas) return;
+  const int r0 = static_cast<int>(static_cast<long long>(units) * blockIdx.x / ctas);
+  const int r1 = static_cast<int>(static_cast<long long>(units) * (blockIdx.x + 1) / ctas);
+
+  auto stretch_at = [&](int u) {
+    int lo = 0, hi = 255;  // the last run of sequences that begins at or before u and is not empty
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (pre[mid] <= u)
+        lo = mid;
+      else
+        hi = mid - 1;
+    }
+    Stretch x;
+    int b = lo * run, at = pre[lo];
+    x.s = span_of<U::TOK>(a.span, b);
+    while (at + x.s.n * per_seq <= u) {
+      at += x.s.n * per_seq;
+      x.s = span_of<U::TOK>(a.span, ++b);
+    }
+    const int item = (u - at) / x.s.n;
+    x.b = b;
+    x.head = item / a.tiles;
+    x.tile = item - x.head * a.tiles;
+    x.begin = at + item * x.s.n;
+    x.end = x.begin + x.s.n;
+    return x;
+  };
+  auto first_token = [&](const Stretch& x, int u) {
+    const int k = u - x.begin;
+    return (k < x.s.sinks ? k : x.s.lo + k - x.s.sinks) * U::TOK;
+  };
+
+  // ---- this warp's copies, running kStages units ahead; a page id is looked up one unit earlier still
+  Stretch px = stretch_at(r0);
+  int pu = r0 + warp, page_next = 0, tok_next = 0;
+  bool more = true;
+  unsigned bad = 0;  // bit per stage: no such page, the unit's keys are masked
+  auto look_up = [&]() {  // moves to this warp's next unit at or after pu and finds its page
+    while (pu >= min(px.end, r1)) {
+      if (px.end >= r1) {
+        more = false;
+        return;
+      }
+      const int s = px.end;
+      px = stretch_at(s);
+      pu = s + warp;
+    }
+    tok_next = first_token(px, pu);
+    page_next = __ldg(a.c.table + static_cast<size_t>(px.b) * a.c.max_pages + tok_next / kPage);
+  };
+  auto copy = [&](int st) {  // issues the unit that look_up found, then looks up the next
+    if (!more) return;
+    int page = page_next;
+    bad &= ~(1u << st);
+    if (page < 0 || page >= a.c.n_pages) {
+      if (lane == 0 && a.c.err) atomicOr(a.c.err, kErrPage);
+      bad |= 1u << st;
+      page = 0;
+    }
+    if (lane == 0) {
+      const unsigned char* src = a.c.pages + cache4::block_offset<DH>(a.c, page, px.head);
+      const uint32_t dst = ring_s + st * U::BYTES, bar = bars + 8 * st;
+      sm100::mbar_arrive_expect_tx(bar, U::BYTES);
+      if constexpr (U::TOK == kPage) {
+        sm100::bulk_load(dst, src, U::BYTES, bar);
+      } else {
+        using L = cache4::Layout<DH>;
+        const int r = tok_next % kPage;
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+          sm100::bulk_load(dst + v * U::V_OFF, src + v * L::V_OFF + r * L::CODE_ROW, U::CODES, bar);
+          sm100::bulk_load(dst + v * U::V_OFF + U::CODES, src + v * L::V_OFF + L::CODES + r * L::SCALE_ROW, U::SCALES,
+                           bar);
+        }
+      }
+    }
+    pu += kWarps;
+    look_up();
+  };
+  look_up();
+  int issued = 0, used = 0;
+  for (; issued < kStages && more; ++issued) copy(issued);
+
+  bool dead = false;
+  for (int u0 = r0; u0 < r1;) {
+    const Stretch x = stretch_at(u0);
+    const int u1 = min(x.end, r1);
+    const int len = __ldg(a.c.lens + x.b), first_pos = len - a.n_q;
+
+    // ---- the tile's queries: row n of tile j, channels of this lane's share of a key
+    uint32_t q[NT][TERMS][KS][2];
+    float rs[NT][2];   // this lane's two accumulator columns (rows 2t, 2t + 1): score scale in powers of 2
+    int pos[NT][2];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      const int row = (x.tile * NT + j) * 8 + g;
+      const bool on = row < a.rows;
+      const int tok = on ? row / a.group : 0, hd = on ? row - tok * a.group : 0;
+      const T* src = static_cast<const T*>(a.q) + (static_cast<size_t>(x.b) * a.n_q + tok) * a.ldq +
+                     (x.head * a.group + hd) * DH + t * (DH / 4);
+      float f[DH / 4];
+      float amax = 0.f;
+      bool fin = true;
+#pragma unroll
+      for (int i = 0; i < DH / 4; ++i) {
+        f[i] = on ? to_f32(src[i]) : 0.f;
+        fin &= fabsf(f[i]) <= 3.4028235e38f;
+        amax = fmaxf(amax, fabsf(f[i]));
+      }
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+      fin = __shfl_xor_sync(0xffffffffu, fin, 1) && fin;
+      fin = __shfl_xor_sync(0xffffffffu, fin, 2) && fin;
+      // the row's largest magnitude to 2^10 .. 2^11
+      const int e = min(max(static_cast<int>(__float_as_uint(amax) >> 23) - 127, -110), 127);
+      const float up = amax > 0.f ? __uint_as_float(static_cast<uint32_t>(127 + 10 - e) << 23) : 1.f;
+      const float down = amax > 0.f ? __uint_as_float(static_cast<uint32_t>(127 - 10 + e) << 23) : 1.f;
+#pragma unroll
+      for (int w = 0; w < WK; ++w)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float v0 = f[8 * w + i] * up, v1 = f[8 * w + i + 4] * up;
+          q[j][0][2 * w + (i >> 1)][i & 1] = pack2<__half>(v0, v1);
+          if constexpr (SPLIT) q[j][1][2 * w + (i >> 1)][i & 1] = pack2<__half>(lo_term<__half>(v0), lo_term<__half>(v1));
+        }
+      const float scale = fin ? down * (kCodeScale * rsqrtf(static_cast<float>(DH)) * 1.4426950408889634f) : NAN;
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        rs[j][c] = __shfl_sync(0xffffffffu, scale, 4 * (2 * t + c));
+        pos[j][c] = __shfl_sync(0xffffffffu, first_pos + tok, 4 * (2 * t + c));
+      }
+    }
+
+    float o[NT][MU][4], m[NT][2], l[NT][2];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      m[j][0] = m[j][1] = -INFINITY;
+      l[j][0] = l[j][1] = 0.f;
+#pragma unroll
+      for (int i = 0; i < MU; ++i) o[j][i][0] = o[j][i][1] = o[j][i][2] = o[j][i][3] = 0.f;
+    }
+
+    for (int u = u0 + warp; u < u1; u += kWarps) {
+      const int st = used % kStages;
+      const int key0 = first_token(x, u);
+      const bool gone = (bad >> st) & 1u;
+      const unsigned char* const kc = ring + st * U::BYTES;
+      if (!sm100::mbar_wait(bars + 8 * st, (used / kStages) & 1, abort_flag)) dead = true;
+      // S^T: keys g and g + 8 of each tile sit at rows (g >> 1) + 4 (g & 1) and 8 further
+      const int rk = (g >> 1) + 4 * (g & 1);
+      float s[MT][NT][4];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+        for (int j = 0; j < NT; ++j) s[mt][j][0] = s[mt][j][1] = s[mt][j][2] = s[mt][j][3] = 0.f;
+        uint32_t w[2][WK];
+        uint32_t sb[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int r = 16 * mt + rk + 8 * h;
+          lds_words<WK>(kc + r * (DH / 2) + t * (DH / 8), w[h]);
+          const unsigned char* sp = kc + U::CODES + r * (DH / 16);
+          if constexpr (DH == 128)
+            sb[h] = *reinterpret_cast<const unsigned short*>(sp + 2 * t);
+          else
+            sb[h] = sp[DH == 64 ? t : t >> 1];
+        }
+        __half2 sc[2], cc[2];
+#pragma unroll
+        for (int i = 0; i < WK; ++i) {
+          if (i == 0 || (DH == 128 && i == 2)) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const uint32_t b = DH == 128 ? (i == 0 ? sb[h] & 255u : sb[h] >> 8) : sb[h];
+              scale_pair(b * 0x10001u, sc[h], cc[h]);
+            }
+          }
+          uint32_t v0[4], v1[4];
+          dequant(w[0][i], sc[0], cc[0], v0);
+          dequant(w[1][i], sc[1], cc[1], v1);
+#pragma unroll
+          for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int e = 0; e < TERMS; ++e) {
+              mma(s[mt][j], v0[0], v1[0], v0[1], v1[1], q[j][e][2 * i][0], q[j][e][2 * i][1]);
+              mma(s[mt][j], v0[2], v1[2], v0[3], v1[3], q[j][e][2 * i + 1][0], q[j][e][2 * i + 1][1]);
+            }
+        }
+      }
+      // mask: units that hold keys after some row's position, or before some row's window
+      const int behind = len - key0;  // rows of the unit that hold tokens
+      const bool edge = gone || key0 + U::TOK - 1 > first_pos ||
+                        (len - 1 - key0 >= a.span.window && key0 + U::TOK > a.span.sinks);
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) s[mt][j][i] *= rs[j][i & 1];
+      if (edge) {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int key = key0 + 16 * mt + rk + 8 * (i >> 1), p = pos[j][i & 1];
+              if (gone || key > p || (p - key >= a.span.window && key >= a.span.sinks)) s[mt][j][i] = -INFINITY;
+            }
+      }
+      uint32_t pb[MT][NT][TERMS][2];
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        float ref[2], corr[2];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          float mx = fmaxf(s[0][j][c], s[0][j][c + 2]);
+#pragma unroll
+          for (int mt = 1; mt < MT; ++mt) mx = fmaxf(mx, fmaxf(s[mt][j][c], s[mt][j][c + 2]));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+          const float mn = fmaxf(m[j][c], mx);
+          ref[c] = mn == -INFINITY ? 0.f : mn;  // nothing seen yet: weights 2^-inf = 0
+          corr[c] = ex2(m[j][c] - ref[c]);
+          m[j][c] = mn;
+          l[j][c] *= corr[c];
+          ref[c] -= 15.f;
+        }
+        if (__any_sync(0xffffffffu, corr[0] != 1.f || corr[1] != 1.f)) {
+#pragma unroll
+          for (int i = 0; i < MU; ++i) {
+            o[j][i][0] *= corr[0], o[j][i][1] *= corr[1];
+            o[j][i][2] *= corr[0], o[j][i][3] *= corr[1];
+          }
+        }
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          float p[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            p[i] = ex2(s[mt][j][i] - ref[i & 1]);
+            l[j][i & 1] += p[i];
+          }
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            pb[mt][j][0][h] = transpose8(pack2<__half>(p[2 * h], p[2 * h + 1]));
+            if constexpr (SPLIT)
+              pb[mt][j][1][h] = transpose8(pack2<__half>(lo_term<__half>(p[2 * h]), lo_term<__half>(p[2 * h + 1])));
+          }
+        }
+      }
+      // O^T += V^T P^T: keys 2t, 2t + 1, 2t + 8, 2t + 9 of a tile sit at rows t, t + 4, t + 8, t + 12
+      const unsigned char* const vc = kc + U::V_OFF;
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        constexpr int WV = DH == 128 ? 2 : 1;
+        uint32_t w[4][WV], sb[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int r = 16 * mt + t + 4 * k;
+          if constexpr (DH == 32)
+            w[k][0] = *reinterpret_cast<const unsigned short*>(vc + r * (DH / 2) + 2 * g);
+          else
+            lds_words<WV>(vc + r * (DH / 2) + g * (DH / 16), w[k]);
+          sb[k] = vc[U::CODES + r * (DH / 16) + (DH == 128 ? g : DH == 64 ? g >> 1 : g >> 2)];
+          if (edge && (gone || r >= behind)) sb[k] = 0;  // no token there: bytes of any kind
+        }
+        __half2 sa, ca, sz, cz;
+        scale_pair(sb[0] | (sb[1] << 16), sa, ca);
+        scale_pair(sb[2] | (sb[3] << 16), sz, cz);
+#pragma unroll
+        for (int i = 0; i < WV; ++i)
+#pragma unroll
+          for (int half = 0; half < (DH == 32 ? 1 : 2); ++half) {
+            const uint32_t sel = half ? 0x7632u : 0x5410u;  // channels 4 half .. of both keys
+            uint32_t v0[4], v1[4];
+            dequant(__byte_perm(w[0][i], w[1][i], sel), sa, ca, v0);
+            dequant(__byte_perm(w[2][i], w[3][i], sel), sz, cz, v1);
+            const int mu = 4 * i + 2 * half;
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+              for (int e = 0; e < TERMS; ++e) {
+                mma(o[j][mu], v0[0], v0[1], v1[0], v1[1], pb[mt][j][e][0], pb[mt][j][e][1]);
+                mma(o[j][mu + 1], v0[2], v0[3], v1[2], v1[3], pb[mt][j][e][0], pb[mt][j][e][1]);
+              }
+          }
+      }
+      __syncwarp();  // every lane has read the stage
+      ++used;
+      if (more) {
+        copy(st);
+        ++issued;
+      }
+    }
+
+    // ---- the warps' results of this stretch, added
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        l[j][c] += __shfl_xor_sync(0xffffffffu, l[j][c], 4);
+        l[j][c] += __shfl_xor_sync(0xffffffffu, l[j][c], 8);
+        l[j][c] += __shfl_xor_sync(0xffffffffu, l[j][c], 16);
+        if (g == 0) {
+          ml[warp * 8 * NT + 8 * j + 2 * t + c] = m[j][c];
+          ml[(kWarps + warp) * 8 * NT + 8 * j + 2 * t + c] = l[j][c];
+        }
+      }
+    const bool whole = u0 == x.begin && u1 == x.end;
+    float* const part = a.parts + static_cast<size_t>(2 * blockIdx.x + (u0 == r0 ? 0 : 1)) * (DH + 2) * 8 * NT;
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      __syncthreads();
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        float top = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, ml[w * 8 * NT + 8 * j + 2 * t + c]);
+        const float by = top == -INFINITY && m[j][c] == top ? (l[j][c] == l[j][c] ? 0.f : NAN) : ex2(m[j][c] - top);
+#pragma unroll
+        for (int i = 0; i < MU; ++i)
+          *reinterpret_cast<float2*>(merge + (warp * 8 + 2 * t + c) * S::LD + g * (DH / 8) + 2 * i) =
+              make_float2(o[j][i][c] * by, o[j][i][c + 2] * by);
+      }
+      __syncthreads();
+      for (int e = threadIdx.x; e < 8 * DH / 4; e += 32 * kWarps) {
+        const int row = e / (DH / 4), ch = (e - row * (DH / 4)) * 4;
+        float top = -INFINITY, sum = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, ml[w * 8 * NT + 8 * j + row]);
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          const float lw = ml[(kWarps + w) * 8 * NT + 8 * j + row], mw = ml[w * 8 * NT + 8 * j + row];
+          sum += mw == -INFINITY ? lw * 0.f : lw * ex2(mw - top);  // 0, or NaN of a query that is not finite
+          const float4 v = *reinterpret_cast<const float4*>(merge + (w * 8 + row) * S::LD + ch);
+          acc.x += v.x, acc.y += v.y, acc.z += v.z, acc.w += v.w;
+        }
+        const int rr = (x.tile * NT + j) * 8 + row;
+        if (whole) {
+          if (rr < a.rows) {
+            const int tok = rr / a.group, hd = rr - tok * a.group;
+            T* dst = static_cast<T*>(a.out) +
+                     ((static_cast<size_t>(x.b) * a.n_q + tok) * a.H + x.head * a.group + hd) * DH + ch;
+            const float inv = sum == 0.f ? 0.f : kCodeScale / sum;
+            if constexpr (SPLIT)
+              *reinterpret_cast<float4*>(dst) = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+            else
+              *reinterpret_cast<uint2*>(dst) =
+                  make_uint2(pack2<T>(acc.x * inv, acc.y * inv), pack2<T>(acc.z * inv, acc.w * inv));
+          }
+        } else {
+          *reinterpret_cast<float4*>(part + (8 * j + row) * DH + ch) = acc;
+          if (ch == 0) {
+            part[8 * NT * DH + 8 * j + row] = top;
+            part[8 * NT * (DH + 1) + 8 * j + row] = sum;
+          }
+        }
+      }
+    }
+    __syncthreads();  // ml and merge may be written again
+    u0 = u1;
+  }
+  if (dead) {
+    if (lane == 0 && a.c.err) atomicOr(a.c.err, kErrTimeoutEpilogue);
+    for (int k = max(used - kStages, 0); k < issued; ++k) sm100::mbar_wait_drain(bars + 8 * (k % kStages), (k / kStages) & 1);
+  }
+}
+
+// Rows of items that several CTAs shared: their parts added in the order of the keys. Rows that
+// see nothing: zeros. One CTA per (sequence, kv head, row tile), one warp per row.
+template <int DH, typename T, int NT>
+__global__ void __launch_bounds__(32 * 8 * NT) cache_attn_join_kernel(const DecodeArgs a, int max_ctas) {
+  pdl_trigger();
+  pdl_wait();
+  const int tile = blockIdx.x % a.tiles, head = (blockIdx.x / a.tiles) % a.c.Hkv, b = blockIdx.x / (a.tiles * a.c.Hkv);
+  const int units = a.prefix[a.c.n_seqs], at = a.prefix[b];
+  const int n = (a.prefix[b + 1] - at) / (a.c.Hkv * a.tiles);
+  const int row = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rr = tile * 8 * NT + row;
+  if (rr >= a.rows) return;
+  const int tok = rr / a.group, hd = rr - tok * a.group;
+  T* dst = static_cast<T*>(a.out) + ((static_cast<size_t>(b) * a.n_q + tok) * a.H + head * a.group + hd) * DH;
+  constexpr int C = DH / 32;
+  float acc[C];
+#pragma unroll
+  for (int i = 0; i < C; ++i) acc[i] = 0.f;
+  float sum = 0.f;
+  if (n > 0) {
+    const int begin = at + (head * a.tiles + tile) * n, end = begin + n;
+    const int ctas = min(max_ctas, (units + kWarps - 1) / kWarps);
+    auto cta_of = [&](int u) {
+      return static_cast<int>((static_cast<long long>(u + 1) * ctas - 1) / units);
+    };
+    const int w0 = cta_of(begin), w1 = cta_of(end - 1);
+    if (w0 == w1) return;  // that CTA wrote the result
+    auto part_of = [&](int w) {
+      const int r0 = static_cast<int>(static_cast<long long>(units) * w / ctas);
+      return a.parts + static_cast<size_t>(2 * w + (max(begin, r0) == r0 ? 0 : 1)) * (DH + 2) * 8 * NT;
+    };
+    float top = -INFINITY;
+    for (int w = w0 + lane; w <= w1; w += 32) top = fmaxf(top, part_of(w)[8 * NT * DH + row]);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    for (int w = w0; w <= w1; ++w) {
+      const float* p = part_of(w);
+      const float mw = p[8 * NT * DH + row], lw = p[8 * NT * (DH + 1) + row];
+      const float by = mw == -INFINITY ? 0.f : ex2(mw - top);
+      sum += lw * by;
+#pragma unroll
+      for (int i = 0; i < C; ++i) acc[i] = fmaf(p[row * DH + 32 * i + lane], by, acc[i]);
+    }
+  }
+  const float inv = sum == 0.f ? 0.f : kCodeScale / sum;
+#pragma unroll
+  for (int i = 0; i < C; ++i) dst[32 * i + lane] = from_f32<T>(acc[i] * inv);
+}
+
+int tile_rows(int rows, bool bf16) { return bf16 && rows > 8 ? 16 : 8; }
+
+// Most units a call may have, and the CTAs for them
+long long most_units(int n_seqs, int max_pages, int n_q, int tiles, int Hkv, int dh, int window, int sinks) {
+  const int tok = dh == 128 ? 32 : 64;
+  const long long all = static_cast<long long>(max_pages) * kPage / tok;
+  // a window and the tokens before it cross at most one more unit than they fill
+  const long long seen = (static_cast<long long>(window) + n_q + tok - 2) / tok + 1 + (sinks + tok - 1LL) / tok;
+  return static_cast<long long>(n_seqs) * Hkv * tiles * (all < seen ? all : seen);
+}
+int cta_count(long long units) {
+  const long long c = (units + kWarps - 1) / kWarps;
+  return static_cast<int>(c < kMaxCtas ? c : kMaxCtas);
+}
+
+template <int DH, typename T, int NT>
+cudaError_t launch_decode(const CacheAttnArgs& c, cudaStream_t st) {
+  using S = DecodeSmem<DH, NT>;
+  constexpr int MINB = DH == 128 && NT == 2 ? 1 : 2;
+  DecodeArgs a{};
+  a.c = c.c;
+  a.span = {c.c.lens, c.c.max_pages * kPage, c.n_q, c.window, c.sinks};
+  a.q = c.q, a.ldq = c.ldq, a.out = c.out;
+  a.n_q = c.n_q, a.H = c.H, a.group = c.H / c.c.Hkv;
+  a.rows = c.n_q * a.group;
+  a.tiles = (a.rows + 8 * NT - 1) / (8 * NT);
+  const int ctas = cta_count(most_units(c.c.n_seqs, c.c.max_pages, c.n_q, a.tiles, c.c.Hkv, DH, c.window, c.sinks));
+  a.parts = static_cast<float*>(c.ws);
+  a.prefix = reinterpret_cast<int*>(a.parts + static_cast<size_t>(2) * ctas * (DH + 2) * 8 * NT);
+  auto kernel = cache_attn_kernel<DH, T, NT, MINB>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::BYTES);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(kernel, dim3(ctas), dim3(32 * kWarps), S::BYTES, st, a);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(cache_attn_join_kernel<DH, T, NT>, dim3(c.c.n_seqs * c.c.Hkv * a.tiles), dim3(32 * 8 * NT), 0, st, a,
+                 ctas);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+template <int DH>
+cudaError_t launch_dh(const CacheAttnArgs& a, bool bf16, cudaStream_t st) {
+  if (!bf16) return launch_decode<DH, float, 1>(a, st);
+  return tile_rows(a.n_q * (a.H / a.c.Hkv), true) == 16 ? launch_decode<DH, __nv_bfloat16, 2>(a, st)
+                                                        : launch_decode<DH, __nv_bfloat16, 1>(a, st);
 }
 
 }  // namespace
 
-size_t cache_attention_workspace(int, int, int, int, int, int, int, int) { return 16; }
+size_t cache_attention_workspace(int n_seqs, int max_pages, int n_q, int H, int Hkv, int dh, int window, int sinks) {
+  // the larger of what either type needs: its tiles decide how many parts there are, and their size
+  size_t most = 0;
+  const int rows = n_q * (H / Hkv);
+  for (int bf16 = 0; bf16 < 2; ++bf16) {
+    const int tr = tile_rows(rows, bf16), tiles = (rows + tr - 1) / tr;
+    const long long units = most_units(n_seqs, max_pages, n_q, tiles, Hkv, dh, window, sinks);
+    if (units > 0x7fffffffLL) return 0;
+    const size_t bytes = static_cast<size_t>(2) * cta_count(units) * (dh + 2) * tr * 4;
+    most = bytes > most ? bytes : most;
+  }
+  return most + (static_cast<size_t>(n_seqs) + 1) * 4;
+}
 
 cudaError_t launch_cache_attention(const CacheAttnArgs& a, int dh, bool bf16, cudaStream_t st) {
   switch (dh) {
-    case 32: return bf16 ? launch_simple<32, __nv_bfloat16>(a, st) : launch_simple<32, float>(a, st);
-    case 64: return bf16 ? launch_simple<64, __nv_bfloat16>(a, st) : launch_simple<64, float>(a, st);
-    case 128: return bf16 ? launch_simple<128, __nv_bfloat16>(a, st) : launch_simple<128, float>(a, st);
+    case 32: return launch_dh<32>(a, bf16, st);
+    case 64: return launch_dh<64>(a, bf16, st);
+    case 128: return launch_dh<128>(a, bf16, st);
   }
   return cudaErrorInvalidValue;
 }

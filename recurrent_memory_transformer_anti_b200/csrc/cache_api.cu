@@ -119,12 +119,12 @@ rmt_status rmt_cache_read(const rmt_cache* c, void* k, void* v, int64_t ld, int3
 }
 
 size_t rmt_attention_cache_workspace(const rmt_cache* c, int32_t n_q, int32_t H, int32_t window, int32_t sinks) {
-  if (const char* why = attention_problem(c, n_q, H, window, sinks)) {
-    fail(RMT_EINVAL, why);
-    return 0;
-  }
-  return cache_attention_workspace(c->n_seqs, c->max_pages, n_q, H, c->n_kv_heads, c->head_dim,
-                                   window_length(window), sinks);
+  const char* why = attention_problem(c, n_q, H, window, sinks);
+  const size_t n = why ? 0
+                       : cache_attention_workspace(c->n_seqs, c->max_pages, n_q, H, c->n_kv_heads, c->head_dim,
+                                                   window_length(window), sinks);
+  if (n == 0) fail(RMT_EINVAL, why ? why : "the sequences hold too many pages for one call");
+  return n;
 }
 
 rmt_status rmt_attention_cache(const rmt_cache* c, const void* q, int64_t ldq, void* out, int32_t n_q, int32_t H,
@@ -137,7 +137,9 @@ rmt_status rmt_attention_cache(const rmt_cache* c, const void* q, int64_t ldq, v
   if (ldq < int64_t(H) * c->head_dim) return fail(RMT_EINVAL, "ldq is below H * head_dim");
   if (!aligned(q, 16) || !aligned(out, 16) || (ldq * es) % 16 || !aligned(workspace, 16))
     return fail(RMT_EINVAL, "q, its rows, out and workspace must be 16-byte aligned");
-  if (workspace_bytes < rmt_attention_cache_workspace(c, n_q, H, window, sinks))
+  const size_t need = rmt_attention_cache_workspace(c, n_q, H, window, sinks);
+  if (need == 0) return RMT_EINVAL;
+  if (workspace_bytes < need)
     return fail(RMT_EINVAL, "the workspace is smaller than rmt_attention_cache_workspace asks for");
   OnDeviceOf dev(c->pages);
   if (dev.st != RMT_OK) return dev.st;

@@ -490,7 +490,11 @@ def test_captured_calls_replay_with_new_lengths_and_inputs(cuda_ok):
         s.pages.copy_(before)
         step()
         rmt.rmt_sync(None)
-        assert torch.equal(got, out) and torch.equal(wgot, wout) and torch.equal(pages, s.pages)
+        # as bits: from the second replay on the lengths take in tokens that no call has written, whose
+        # bytes may stand for NaN
+        bits = [x.view(torch.int16) for x in (got, out, wgot, wout)]
+        assert torch.equal(*bits[:2]) and torch.equal(*bits[2:]) and torch.equal(pages, s.pages)
+        assert it > 0 or torch.isfinite(out).all()
 
 
 @gpu
