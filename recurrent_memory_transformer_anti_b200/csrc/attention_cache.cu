@@ -15,7 +15,7 @@
 // (mma.sync m16n8k16, f16 operands, fp32 sums: the codes turn into operands in registers, and tcgen05
 // would have them pass through shared memory again, four times their bytes). A code's nibble
 // or-ed into the f16 pattern of 64 is 64 + (q + 8); times the scale minus 72 scales is q * scale,
-// exact, in one fused operation for two codes. Scales are taken at 2^-4 of their value so that 72 of
+// exact, in one fused operation for two codes (dequant). Scales are taken at 2^-4 of their value so that 72 of
 // them stay in f16's range; the factor comes back with the row's scale and at the end. A lane takes 16
 // (or 8, or 32) consecutive channels of a key, since the order of a dot product's terms is free as long as
 // Q has the same one, and for V eight neighbouring lanes' keys are chosen so that the reads of a warp are
@@ -98,18 +98,37 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
   return r;
 }
 
-// Two scale bytes (low and high half of b) as f16 pairs: 2^-4 of the scales, and -72 times that.
-__device__ __forceinline__ void scale_pair(uint32_t b, __half2& s, __half2& c) {
-  s = __hmul2(as_h2(b << 7), __float2half2_rn(1.f / kCodeScale));
-  c = __hmul2(s, __float2half2_rn(-72.f));
+// Two scale bytes (low and high half of b) as f16 pairs: 2^-4 of the scales (x), -72 (y) and -8
+// (z) times that.
+struct Scale {
+  __half2 x, y, z;
+};
+__device__ __forceinline__ Scale scale_pair(uint32_t b) {
+  Scale s;
+  s.x = __hmul2(as_h2(b << 7), __float2half2_rn(1.f / kCodeScale));
+  s.y = __hmul2(s.x, __float2half2_rn(-72.f));
+  s.z = __hmul2(s.x, __float2half2_rn(-8.f));
+  return s;
 }
-// The codes j of the low and of the high half of w, j = 0..3, times their scales.
-__device__ __forceinline__ void dequant(uint32_t w, __half2 s, __half2 c, uint32_t (&v)[4]) {
-  const uint32_t m = 0x00F000F0u, one = 0x54005400u;
-  v[0] = h2(__hfma2(as_h2(((w << 4) & m) | one), s, c));
-  v[1] = h2(__hfma2(as_h2((w & m) | one), s, c));
-  v[2] = h2(__hfma2(as_h2(((w >> 4) & m) | one), s, c));
-  v[3] = h2(__hfma2(as_h2(((w >> 8) & m) | one), s, c));
+__device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+  return r;
+}
+// The codes j of the low and of the high half of w, j = 0..3, times their scales. A byte's high
+// nibble h sits where it counts units of 64's f16 pattern: 64 + h; the byte in 1024's: 1024 + l + 16 h,
+// less 16 (64 + h) is its low nibble. That takes one shift per word instead of three (shifts and
+// logic run at half the rate of the fused multiply-adds, and are what bounds the kernel).
+__device__ __forceinline__ void dequant(uint32_t w, const Scale& s, uint32_t (&v)[4]) {
+  const __half2 less = __float2half2_rn(-16.f);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const __half2 h = as_h2(and_or(w, 0x00F000F0u, 0x54005400u));
+    const __half2 l = __hfma2(h, less, as_h2(and_or(w, 0x00FF00FFu, 0x64006400u)));
+    v[2 * i] = h2(__hfma2(l, s.x, s.z));
+    v[2 * i + 1] = h2(__hfma2(h, s.x, s.y));
+    w >>= 8;
+  }
 }
 
 template <int N>
@@ -243,16 +262,12 @@ __global__ void __launch_bounds__(32 * kWarps, MINB) cache_attn_kernel(const Dec
   int pu = r0 + warp, page_next = 0, tok_next = 0;
   bool more = true;
   unsigned bad = 0;  // bit per stage: no such page, the unit's keys are masked
-  auto look_up = [&]() {  // moves to this warp's next unit at or after pu and finds its page
-    while (pu >= min(px.end, r1)) {
-      if (px.end >= r1) {
-        more = false;
-        return;
-      }
-      const int s = px.end;
-      px = stretch_at(s);
-      pu = s + warp;
+  auto look_up = [&]() {  // finds the page of unit pu
+    if (pu >= r1) {
+      more = false;
+      return;
     }
+    if (pu >= px.end) px = stretch_at(pu);
     tok_next = first_token(px, pu);
     page_next = __ldg(a.c.table + static_cast<size_t>(px.b) * a.c.max_pages + tok_next / kPage);
   };
@@ -290,6 +305,7 @@ __global__ void __launch_bounds__(32 * kWarps, MINB) cache_attn_kernel(const Dec
   for (; issued < kStages && more; ++issued) copy(issued);
 
   bool dead = false;
+  int u = r0 + warp;  // this warp's units: every eighth of the share
   for (int u0 = r0; u0 < r1;) {
     const Stretch x = stretch_at(u0);
     const int u1 = min(x.end, r1);
@@ -310,8 +326,21 @@ __global__ void __launch_bounds__(32 * kWarps, MINB) cache_attn_kernel(const Dec
       float amax = 0.f;
       bool fin = true;
 #pragma unroll
+      for (int i = 0; i < DH / 4; i += 16 / static_cast<int>(sizeof(T))) {  // 16 bytes at a time
+        const uint4 v = on ? *reinterpret_cast<const uint4*>(src + i) : make_uint4(0, 0, 0, 0);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if constexpr (SPLIT) {
+            f[i + k] = __uint_as_float(w[k]);
+          } else {
+            f[i + 2 * k] = __uint_as_float(w[k] << 16);
+            f[i + 2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
+          }
+        }
+      }
+#pragma unroll
       for (int i = 0; i < DH / 4; ++i) {
-        f[i] = on ? to_f32(src[i]) : 0.f;
         fin &= fabsf(f[i]) <= 3.4028235e38f;
         amax = fmaxf(amax, fabsf(f[i]));
       }
@@ -348,7 +377,7 @@ __global__ void __launch_bounds__(32 * kWarps, MINB) cache_attn_kernel(const Dec
       for (int i = 0; i < MU; ++i) o[j][i][0] = o[j][i][1] = o[j][i][2] = o[j][i][3] = 0.f;
     }
 
-    for (int u = u0 + warp; u < u1; u += kWarps) {
+    for (; u < u1; u += kWarps) {
       const int st = used % kStages;
       const int key0 = first_token(x, u);
       const bool gone = (bad >> st) & 1u;
@@ -373,19 +402,19 @@ __global__ void __launch_bounds__(32 * kWarps, MINB) cache_attn_kernel(const Dec
           else
             sb[h] = sp[DH == 64 ? t : t >> 1];
         }
-        __half2 sc[2], cc[2];
+        Scale sc[2];
 #pragma unroll
         for (int i = 0; i < WK; ++i) {
           if (i == 0 || (DH == 128 && i == 2)) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               const uint32_t b = DH == 128 ? (i == 0 ? sb[h] & 255u : sb[h] >> 8) : sb[h];
-              scale_pair(b * 0x10001u, sc[h], cc[h]);
+              sc[h] = scale_pair(b * 0x10001u);
             }
           }
           uint32_t v0[4], v1[4];
-          dequant(w[0][i], sc[0], cc[0], v0);
-          dequant(w[1][i], sc[1], cc[1], v1);
+          dequant(w[0][i], sc[0], v0);
+          dequant(w[1][i], sc[1], v1);
 #pragma unroll
           for (int j = 0; j < NT; ++j)
 #pragma unroll
@@ -399,12 +428,6 @@ __global__ void __launch_bounds__(32 * kWarps, MINB) cache_attn_kernel(const Dec
       const int behind = len - key0;  // rows of the unit that hold tokens
       const bool edge = gone || key0 + U::TOK - 1 > first_pos ||
                         (len - 1 - key0 >= a.span.window && key0 + U::TOK > a.span.sinks);
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int j = 0; j < NT; ++j)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) s[mt][j][i] *= rs[j][i & 1];
       if (edge) {
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
@@ -430,10 +453,9 @@ __global__ void __launch_bounds__(32 * kWarps, MINB) cache_attn_kernel(const Dec
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
           const float mn = fmaxf(m[j][c], mx);
           ref[c] = mn == -INFINITY ? 0.f : mn;  // nothing seen yet: weights 2^-inf = 0
-          corr[c] = ex2(m[j][c] - ref[c]);
+          corr[c] = ex2((m[j][c] - ref[c]) * rs[j][c]);
           m[j][c] = mn;
           l[j][c] *= corr[c];
-          ref[c] -= 15.f;
         }
         if (__any_sync(0xffffffffu, corr[0] != 1.f || corr[1] != 1.f)) {
 #pragma unroll
@@ -447,7 +469,8 @@ __global__ void __launch_bounds__(32 * kWarps, MINB) cache_attn_kernel(const Dec
           float p[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            p[i] = ex2(s[mt][j][i] - ref[i & 1]);
+            // the difference first: exact for the largest, however large the scores are
+            p[i] = ex2(fmaf(s[mt][j][i] - ref[i & 1], rs[j][i & 1], 15.f));
             l[j][i & 1] += p[i];
           }
 #pragma unroll
@@ -474,17 +497,15 @@ __global__ void __launch_bounds__(32 * kWarps, MINB) cache_attn_kernel(const Dec
           sb[k] = vc[U::CODES + r * (DH / 16) + (DH == 128 ? g : DH == 64 ? g >> 1 : g >> 2)];
           if (edge && (gone || r >= behind)) sb[k] = 0;  // no token there: bytes of any kind
         }
-        __half2 sa, ca, sz, cz;
-        scale_pair(sb[0] | (sb[1] << 16), sa, ca);
-        scale_pair(sb[2] | (sb[3] << 16), sz, cz);
+        const Scale sa = scale_pair(sb[0] + sb[1] * 0x10000u), sz = scale_pair(sb[2] + sb[3] * 0x10000u);
 #pragma unroll
         for (int i = 0; i < WV; ++i)
 #pragma unroll
           for (int half = 0; half < (DH == 32 ? 1 : 2); ++half) {
             const uint32_t sel = half ? 0x7632u : 0x5410u;  // channels 4 half .. of both keys
             uint32_t v0[4], v1[4];
-            dequant(__byte_perm(w[0][i], w[1][i], sel), sa, ca, v0);
-            dequant(__byte_perm(w[2][i], w[3][i], sel), sz, cz, v1);
+            dequant(__byte_perm(w[0][i], w[1][i], sel), sa, v0);
+            dequant(__byte_perm(w[2][i], w[3][i], sel), sz, v1);
             const int mu = 4 * i + 2 * half;
 #pragma unroll
             for (int j = 0; j < NT; ++j)
@@ -511,6 +532,7 @@ __global__ void __launch_bounds__(32 * kWarps, MINB) cache_attn_kernel(const Dec
         l[j][c] += __shfl_xor_sync(0xffffffffu, l[j][c], 4);
         l[j][c] += __shfl_xor_sync(0xffffffffu, l[j][c], 8);
         l[j][c] += __shfl_xor_sync(0xffffffffu, l[j][c], 16);
+        m[j][c] *= rs[j][c];  // in powers of 2
         if (g == 0) {
           ml[warp * 8 * NT + 8 * j + 2 * t + c] = m[j][c];
           ml[(kWarps + warp) * 8 * NT + 8 * j + 2 * t + c] = l[j][c];

@@ -132,47 +132,44 @@ __device__ __forceinline__ Half half_of(const WtArgs& a, const Item& m, int x) {
   h.hi1 = h.b1 + d;
   return h;
 }
-__device__ __forceinline__ bool needs(const WtArgs& a, const Half& h, int t) {
-  return h.on && 128 * t <= h.hi1 && (128 * t + 127 >= h.lo0 || 128 * t < a.sinks);
-}
 // Some row of the item sees only part of tile t.
 __device__ __forceinline__ bool partial(const WtArgs& a, const Item& m, int t) {
   const int u0 = 128 * t, k0 = m.lo + u0 - m.sp;
   return u0 < m.sp || k0 + 127 > m.a0 || m.last - k0 >= a.window;
 }
 
-// The tiles of this CTA's items in order; tau numbers them (ring stages).
+// The tiles of this CTA's items in order, from before the first; tau numbers them (ring stages).
 struct Walk {
   int it, t, tau;
-  bool valid;
   Item m;
-  Half h[2];
-  __device__ __forceinline__ void load(const WtArgs& a) {
-    while (it < a.items) {
-      m = item_of(a, it);
-      if (m.nt > 0) break;
-      it += gridDim.x;
-    }
-    valid = it < a.items;
-    if (valid) {
-      h[0] = half_of(a, m, 0);
-      h[1] = half_of(a, m, 1);
-    }
+  __device__ __forceinline__ Walk() : it(static_cast<int>(blockIdx.x) - static_cast<int>(gridDim.x)), t(0), tau(-1) {
+    m.nt = 0;
   }
-  __device__ __forceinline__ void begin(const WtArgs& a) {
-    it = blockIdx.x;
-    t = tau = 0;
-    load(a);
-  }
-  __device__ __forceinline__ void next(const WtArgs& a) {
+  // to the next tile; false past the last
+  __device__ __forceinline__ bool next(const WtArgs& a) {
     ++t;
     ++tau;
-    if (t < m.nt) return;
+    if (t < m.nt) return true;
     t = 0;
-    it += gridDim.x;
-    load(a);
+    do {
+      it += gridDim.x;
+      if (it >= a.items) return false;
+      m = item_of(a, it);
+    } while (m.nt == 0);
+    return true;
   }
 };
+// Tiles that a half needs: f .. l, and those of the sinks.
+struct Need {
+  int f, l;
+};
+__device__ __forceinline__ Need need_of(const WtArgs& a, const Item& m, int x) {
+  const Half h = half_of(a, m, x);
+  return {h.lo0 / 128, h.on ? h.hi1 / 128 : -1};
+}
+__device__ __forceinline__ bool needs(const WtArgs& a, const Need& n, int t) {
+  return t <= n.l && (t >= n.f || 128 * t < a.sinks);
+}
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
@@ -198,6 +195,11 @@ __device__ __forceinline__ void add_pair(float& x, float& y, float a, float b) {
       "add.rn.f32x2 p, p, q;\n\tmov.b64 {%0, %1}, p;\n\t}"
       : "+f"(x), "+f"(y)
       : "f"(a), "f"(b));
+}
+__device__ __forceinline__ void sub_pair(uint32_t& a, uint32_t& b, float c) {
+  float x = __uint_as_float(a), y = __uint_as_float(b);
+  add_pair(x, y, -c, -c);
+  a = __float_as_uint(x), b = __float_as_uint(y);
 }
 __device__ __forceinline__ float u2f(uint32_t u) { return __uint_as_float(u); }
 
@@ -241,7 +243,6 @@ __global__ void __launch_bounds__(384, 1)
       bool ok = true;
       int nq[2] = {0, 0}, nk = 0, nv = 0;  // loads issued: Q tiles of A and B, K tiles, V tiles
       Walk w;
-      w.begin(a);
       // rows u0 .. u0 + 127 of the item's keys (column col of the packed rows) into a ring tile
       auto load_tile = [&](uint32_t dst, uint32_t full, int col) {
         sm100::mbar_arrive_expect_tx(full, C::TILE);
@@ -260,10 +261,11 @@ __global__ void __launch_bounds__(384, 1)
           r += n;
         }
       };
-      while (w.valid && ok) {
+      while (w.next(a)) {
         if (w.t == 0) {
           for (int x = 0; x < 2 && ok; ++x) {
-            if (!w.h[x].on) continue;
+            const int b0 = w.m.a0 + x * a.tq;
+            if (b0 >= w.m.T) continue;
             const int qs = nq[x] % C::QST, id = x * C::QST + qs;
             ok = sm100::mbar_wait(bar(C::QEMPTY + id), ((nq[x] / C::QST) & 1) ^ 1u, abort_flag);
             if (!ok) break;
@@ -271,7 +273,7 @@ __global__ void __launch_bounds__(384, 1)
             for (int hh = 0; hh < w.m.nh; ++hh)
               for (int sb = 0; sb < C::NSUB; ++sb)
                 sm100::tma_load_3d(base + C::Q_OFF + id * C::TILE + sb * C::SUB + hh * a.tq * 128, &maps.q,
-                                   (w.m.h0 + hh) * HD + 64 * sb, w.h[x].b0, w.m.g, bar(C::QFULL + id));
+                                   (w.m.h0 + hh) * HD + 64 * sb, b0, w.m.g, bar(C::QFULL + id));
             ++nq[x];
           }
           if (!ok) break;
@@ -286,7 +288,6 @@ __global__ void __launch_bounds__(384, 1)
         if (!ok) break;
         load_tile(base + C::V_OFF + st * C::TILE, bar(C::VFULL + st), (a.H + a.Hkv + w.m.kvh) * HD);
         ++nv;
-        w.next(a);
       }
       if (!ok) {
         if (a.err) atomicOr(a.err, kErrTimeoutProducer);
@@ -305,18 +306,17 @@ __global__ void __launch_bounds__(384, 1)
       constexpr uint32_t idS = sm100::idesc_f32acc(128, 128, OpFormat<bf16>::value);
       constexpr uint32_t idO = sm100::idesc_f32acc_bmn(128, HD, OpFormat<bf16>::value);
       bool ok = true;
-      int nq[2] = {-1, -1};  // this tile's Q, counted
+      int nq[2] = {-1, -1};                          // the Q tile in use, counted
       int ns[2] = {0, 0}, np[2] = {0, 0}, no[2] = {0, 0};  // S issued, P V issued, items begun
-      bool fresh_q[2] = {true, true}, fresh_o[2] = {true, true};
+      bool fresh_q[2] = {true, true}, fresh_o[2] = {true, true};  // the next S / P V is an item's first
       auto wait = [&](int b, uint32_t parity) { return sm100::mbar_wait(bar(b), parity & 1u, abort_flag); };
-      auto issue_s = [&](int x, const Walk& w) -> bool {
-        if (w.t == 0) fresh_q[x] = true;
-        const int st = w.tau % C::KST;
+      auto issue_s = [&](int x, int tau, bool last) -> bool {
+        const int st = tau % C::KST;
         if (fresh_q[x]) ++nq[x];
-        const int qs = nq[x] % C::QST, id = x * C::QST + qs;
+        const int id = x * C::QST + nq[x] % C::QST;
         if (fresh_q[x] && !wait(C::QFULL + id, nq[x] / C::QST)) return false;
         fresh_q[x] = false;
-        if (!wait(C::KFULL + st, w.tau / C::KST)) return false;
+        if (!wait(C::KFULL + st, tau / C::KST)) return false;
         if (!C::OVERLAY && ns[x] > 0 && !wait(C::SFREE + x, ns[x] - 1)) return false;
         sm100::tc_fence_after();
 #pragma unroll
@@ -327,14 +327,13 @@ __global__ void __launch_bounds__(384, 1)
           sm100::mma_bf16(tmem + C::S_COL + 128 * x, ad, bd, idS, k > 0);
         }
         sm100::mma_commit(bar(C::SFULL + x));
-        if (w.t == w.h[x].hi1 / 128) sm100::mma_commit(bar(C::QEMPTY + id));  // the item's last S of x
+        if (last) sm100::mma_commit(bar(C::QEMPTY + id));  // the item's last S of x has read its Q
         ++ns[x];
         return true;
       };
-      auto issue_pv = [&](int x, const Walk& w) -> bool {
-        if (w.t == 0) fresh_o[x] = true;
-        const int st = w.tau % C::KST;
-        if (!wait(C::PREADY + x, np[x]) || !wait(C::VSEEN + st, w.tau / C::KST)) return false;
+      auto issue_pv = [&](int x, int tau) -> bool {
+        const int st = tau % C::KST;
+        if (!wait(C::PREADY + x, np[x]) || !wait(C::VSEEN + st, tau / C::KST)) return false;
         // the first P V of an item overwrites O: the previous item's must have been read
         if (fresh_o[x] && no[x] > 0 && !wait(C::OFREE + x, no[x] - 1)) return false;
         sm100::tc_fence_after();
@@ -350,28 +349,34 @@ __global__ void __launch_bounds__(384, 1)
         ++np[x];
         return true;
       };
-      Walk cur, nxt;
-      cur.begin(a);
-      if (cur.valid) {
-        for (int x = 0; x < 2 && ok; ++x)
-          if (needs(a, cur.h[x], 0)) ok = issue_s(x, cur);
-        if (ok) sm100::mma_commit(bar(C::KEMPTY + cur.tau % C::KST));
-      }
-      // a tile that a half does not need still starts an item for it
-      while (cur.valid && ok) {
-        nxt = cur;
-        nxt.next(a);
-        for (int x = 0; x < 2 && ok; ++x) {
-          if (nxt.valid && nxt.t == 0) fresh_q[x] = true;
-          if (cur.t == 0) fresh_o[x] = true;
-          const bool s = nxt.valid && needs(a, nxt.h[x], nxt.t), p = needs(a, cur.h[x], cur.t);
-          if (C::OVERLAY && p) ok = issue_pv(x, cur);
-          if (ok && s) ok = issue_s(x, nxt);
-          if (ok && nxt.valid && x == 1) sm100::mma_commit(bar(C::KEMPTY + nxt.tau % C::KST));
-          if (!C::OVERLAY && ok && p) ok = issue_pv(x, cur);
+      // S of the next tile and P V of the current one, for A and B in turn
+      Walk nxt;
+      int ct = 0, ctau = -1;
+      Need cn[2] = {{0, -1}, {0, -1}}, nn[2] = {{0, -1}, {0, -1}};
+      while (ok) {
+        const bool more = nxt.next(a);
+        if (more && nxt.t == 0) {
+          for (int x = 0; x < 2; ++x) {
+            nn[x] = need_of(a, nxt.m, x);
+            fresh_q[x] = true;
+          }
         }
-        if (ok) sm100::mma_commit(bar(C::VEMPTY + cur.tau % C::KST));
-        cur = nxt;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          if (!ok) break;
+          const bool s = more && needs(a, nn[x], nxt.t), p = ctau >= 0 && needs(a, cn[x], ct);
+          if (ct == 0) fresh_o[x] = true;
+          if (C::OVERLAY && p) ok = issue_pv(x, ctau);
+          if (ok && s) ok = issue_s(x, nxt.tau, nxt.t == nn[x].l);
+          if (ok && more && x == 1) sm100::mma_commit(bar(C::KEMPTY + nxt.tau % C::KST));
+          if (!C::OVERLAY && ok && p) ok = issue_pv(x, ctau);
+        }
+        if (ok && ctau >= 0) sm100::mma_commit(bar(C::VEMPTY + ctau % C::KST));
+        if (!more) break;
+        ct = nxt.t;
+        ctau = nxt.tau;
+        cn[0] = nn[0];
+        cn[1] = nn[1];
       }
       if (!ok) {
         if (a.err) atomicOr(a.err, kErrTimeoutMma);
@@ -384,7 +389,7 @@ __global__ void __launch_bounds__(384, 1)
     const int c = threadIdx.x - 64;
     bool ok = true;
     Walk w;
-    for (w.begin(a); w.valid; w.next(a)) {
+    while (w.next(a)) {
       const int st = w.tau % C::KST;
       ok = __all_sync(0xffffffffu, sm100::mbar_wait(bar(C::VFULL + st), (w.tau / C::KST) & 1, abort_flag));
       if (!ok) break;
@@ -427,6 +432,7 @@ __global__ void __launch_bounds__(384, 1)
     const uint32_t tS = tmem + loff + C::S_COL + 128 * x, tO = tmem + loff + C::O_COL + HD * x,
                    tP = tmem + loff + C::P_COL + C::P_STEP * x;
     const float sl2 = rsqrtf(static_cast<float>(HD)) * 1.4426950408889634f;  // 1/sqrt(dh) * log2(e)
+    const float raise = 8.f / sl2;  // the running maximum (of the raw scores) is only raised by that much
     const int hh = r / a.tq, tok = r - hh * a.tq;
     bool ok = true;
     int n = 0;    // tiles of x processed so far (barrier phases)
@@ -434,6 +440,7 @@ __global__ void __launch_bounds__(384, 1)
     for (int it = blockIdx.x; it < a.items && ok; it += gridDim.x) {
       const Item m = item_of(a, it);
       const Half h = half_of(a, m, x);
+      const Need need = need_of(a, m, x);
       const int tau0 = tau;
       tau += m.nt;
       if (m.nt == 0 || !h.on) continue;
@@ -443,7 +450,7 @@ __global__ void __launch_bounds__(384, 1)
       float m_use = -3e38f, l = 0.f;
       bool poison = false, first = true;
       for (int t = 0; t < m.nt; ++t) {
-        if (!needs(a, h, t)) continue;
+        if (!needs(a, need, t)) continue;
         ok = __all_sync(0xffffffffu, sm100::mbar_wait(bar(C::SFULL + x), n & 1, abort_flag));
         if (!ok) break;
         if (idle) {  // the same waits and arrivals as the busy warps, in the same order
@@ -503,13 +510,25 @@ __global__ void __launch_bounds__(384, 1)
 #pragma unroll
           for (int i = 0; i < 32; i += 2)
             mxp[(i >> 1) & 3] = max3(mxp[(i >> 1) & 3], u2f(s[q4][i]), u2f(s[q4][i + 1]));
-        const float mx = fmaxf(fmaxf(mxp[0], mxp[1]), fmaxf(mxp[2], mxp[3])) * sl2;
+        const float mx = fmaxf(fmaxf(mxp[0], mxp[1]), fmaxf(mxp[2], mxp[3]));
         float corr = 1.f;
         bool rescale = false;
-        if (mx > m_use + 8.f) {  // a row that has seen nothing keeps -3e38: its weights are 2^-inf = 0
-          corr = ex2(m_use - mx);
+        if (mx > m_use + raise) {  // a row that has seen nothing keeps -3e38: its weights are 2^-inf = 0
+          corr = ex2((m_use - mx) * sl2);
           m_use = mx;
           rescale = !first;
+        }
+        // s * sl2 - m * sl2 in one rounding is off by up to 2^-24 of m * sl2: where scores are that
+        // large the difference is taken first
+        float less = m_use * sl2;
+        const bool far = fabsf(m_use) > 4194304.f;
+        if (__any_sync(0xffffffffu, far)) {
+          const float by = far ? m_use : 0.f;  // the warp's other rows stay as they are
+#pragma unroll
+          for (int q4 = 0; q4 < 4; ++q4)
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) sub_pair(s[q4][i], s[q4][i + 1], by);
+          if (far) less = 0.f;
         }
         if (n > 0) {
           // P V of the tile before must be done before P and O change
@@ -535,7 +554,7 @@ __global__ void __launch_bounds__(384, 1)
         for (int q4 = 0; q4 < 4; ++q4) {
 #pragma unroll
           for (int i = 0; i < 32; i += 2) {
-            fma_pair(s[q4][i], s[q4][i + 1], sl2, -m_use);
+            fma_pair(s[q4][i], s[q4][i + 1], sl2, -less);
             const float p0 = ex2(u2f(s[q4][i])), p1 = ex2(u2f(s[q4][i + 1]));
             add_pair(sp[i & 2], sp[(i & 2) + 1], p0, p1);
             s[q4][i >> 1] = pack2<bf16>(p0, p1);

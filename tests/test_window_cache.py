@@ -394,6 +394,34 @@ def test_window_attention_keeps_masked_values_out(cuda_ok, dtype, bad, dh):
 
 
 @gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_window_attention_of_large_and_small_queries(cuda_ok, dtype):
+    H, Hkv, dh, M = 7, 1, 64, 300
+    gain = torch.tensor([1.0, 1e-30, 20.0, 1e4, 1e8, 1e30, 0.0], device="cuda").repeat_interleave(dh)
+    qkv = normal(61, (1, M, (H + 2 * Hkv) * dh), dtype).float()
+    qkv[..., :H * dh] *= gain
+    qkv = qkv.to(TORCH[dtype])
+    out = torch.zeros(1, M, H * dh, dtype=TORCH[dtype], device="cuda")
+    rmt.rmt_attention_window(qkv, out, 1, M, H, Hkv, dh, 100, 3, dtype=dtype)
+    rmt.rmt_sync(None)
+    x = f64(qkv)[0]
+    q, k, v = (t.reshape(M, -1, dh) for t in np.split(x, [H * dh, (H + Hkv) * dh], axis=1))
+    got, ref = f64(out).reshape(M, H, dh), attend_ref(q, k, v, np.arange(M), 100, 3)
+    small, large = [0, 1, 2, 6], [3, 4, 5]
+    check_attention(got[:, small], ref[:, small], np.abs(v).max(), dtype)
+    # a score s in fp32 is off by at most 64 * 2^-24 of sum |q k|, so weights may differ where two scores
+    # are that close: there the result lies between the values, elsewhere it is the formula's
+    assert np.isfinite(got).all() and (np.abs(got) <= np.abs(v).max() * (1 + 2.0 ** -7)).all()
+    for h in large:
+        s = q[:, h] @ k[:, 0].T / 8
+        s = np.where(visible(np.arange(M), np.arange(M), 100, 3), s, -np.inf)
+        noise = (np.abs(q[:, h]) @ np.abs(k[:, 0]).T).max(1) / 8 * 64 * 2.0 ** -24
+        top = np.sort(s, 1)
+        clear = (noise < 2.0 ** -10) | (np.where(M > 1, top[:, -1] - top[:, -2], np.inf) > 2 * noise + 40)
+        check_attention(got[clear, h], ref[clear, h], np.abs(v).max(), dtype)
+
+
+@gpu
 def test_window_attention_past_32_bits(cuda_ok):
     H, Hkv, dh, M = 64, 16, 128, 360000
     qkv = torch.zeros(2, M, (H + 2 * Hkv) * dh, dtype=torch.bfloat16, device="cuda")
