@@ -1,14 +1,17 @@
 // Attention of a sequence's newest tokens over its pages of the 4-bit key/value cache.
 //
-// One pass over the codes, which is what bounds it: 72 dh bytes per 64 tokens and kv head. The
-// work of a call is a list of units -- 64 tokens of one kv head (32 at head_dim 128: 4608 bytes
-// either way) for one tile of query rows -- sorted by sequence, head, tile and position, leaving out what no
-// row sees between the sinks and the window. Each CTA takes an equal, contiguous share of the list whatever the
-// lengths are (they are read on the device), so one long sequence and many short ones are both
-// spread over all SMs. A CTA's eight warps take the units of an (item, CTA) stretch in turn; each
-// has its own ring of bulk copies and its own running maximum, sum and output, which are added at the
-// end of the stretch. A stretch that is a whole item gives its result; the others go to the
-// workspace, and a second kernel adds them in the order of the keys: no atomics, equal bits.
+// One pass over the codes, which is what bounds it: 72 dh bytes per 64 tokens and kv head. A unit of
+// work is 64 tokens of one kv head (32 at head_dim 128: 4608 bytes either way) for one tile of query
+// rows; an item is what one (sequence, kv head, row tile) sees of the cache, without what lies between
+// the sinks and the window. Two ways of dealing the units, by the most units an item can have:
+//   up to kWholeUnits: a CTA takes whole items, its eight warps every eighth unit, and adds
+//     their results in shared memory: one launch, nothing read before the item's own length.
+//   more: the units of all items form one list (lengths are read on the device), and each warp
+//     of the grid takes an equal, contiguous stretch of it, so that one long sequence and many short
+//     ones are both spread over all SMs, and no warp waits for another. A stretch that holds a whole
+//     item gives its result; parts go to the workspace, and a second kernel adds them in the
+//     order of the keys: no atomics, equal bits.
+// Each warp has its own ring of bulk copies.
 //
 // Arithmetic. Query rows are the MMA's N (8 or 16 rows: the heads of a group, times the tokens),
 // keys or channels its M, so that few rows waste nothing: S^T = K Q^T, O^T = V^T P^T
@@ -33,8 +36,10 @@ namespace {
 using cache4::CacheArgs;
 using cache4::kPage;
 
-constexpr int kWarps = 8, kStages = 2;
-constexpr int kMaxCtas = 296;  // two per SM
+constexpr int kWarps = 8;
+constexpr int kMaxCtas = 296;    // two per SM
+constexpr int kLeastUnits = 4;   // of a warp's stretch
+constexpr int kWholeUnits = 32;  // items up to this many units are not split
 constexpr float kCodeScale = 16.f;  // operands hold 2^-4 of a value
 
 template <int DH>
@@ -50,13 +55,11 @@ struct Span {
   int n, sinks, lo;
 };
 struct SpanArgs {
-  const int* lens;
   int cap;  // tokens a sequence may hold
   int n_q, window, sinks;
 };
 template <int TOK>
-__device__ __forceinline__ Span span_of(const SpanArgs& a, int b) {
-  const int T = __ldg(a.lens + b);
+__device__ __forceinline__ Span span_of(const SpanArgs& a, int T) {
   Span s{0, 0, 0};
   if (T <= 0 || T > a.cap) return s;
   s.lo = max(0, max(T - a.n_q, 0) - a.window + 1) / TOK;
@@ -74,7 +77,23 @@ struct DecodeArgs {
   void* out;
   int n_q, H, group, rows, tiles;  // rows: n_q * group per kv head, in `tiles` tiles
   int* prefix;    // [n_seqs + 1] units before each sequence (workspace; for the second kernel)
-  float* parts;   // [2 * CTAs] stretches: O [dh][rows of a tile], maxima, sums
+  float* parts;   // two per warp: O [rows of a tile][dh], maxima, sums
+};
+
+// The list of units dealt to warps: equal stretches, the first `more` of them one unit longer.
+struct Deal {
+  int warps, units, each, more;
+  __device__ __forceinline__ Deal(int units_, int ctas) {
+    units = units_;
+    warps = max(1, min(ctas * kWarps, (units + kLeastUnits - 1) / kLeastUnits));
+    each = units / warps;
+    more = units - each * warps;
+  }
+  __device__ __forceinline__ int begin(int w) const { return w * each + min(w, more); }
+  __device__ __forceinline__ int warp_of(int u) const {
+    const int cut = more * (each + 1);
+    return u < cut ? u / (each + 1) : more + (u - cut) / each;
+  }
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -144,60 +163,65 @@ __device__ __forceinline__ void lds_words(const unsigned char* p, uint32_t (&w)[
   }
 }
 
-// Stretch of the unit list inside one (sequence, kv head, row tile).
-struct Stretch {
-  int b, head, tile;
-  int begin, end;  // the item's units
+struct Item {
+  int b, head, tile, len;
+  int begin;  // its first unit in the list
   Span s;
 };
 
-template <int DH, int NT>
+template <int DH, int NT, bool WHOLE>
 struct DecodeSmem {
+  static constexpr int STAGES = WHOLE ? 2 : 3;  // of a warp's ring
   static constexpr int RING = 0;
   static constexpr int LD = DH + 4;
-  static constexpr int MERGE = RING + kWarps * kStages * Unit<DH>::BYTES;  // [warp][8][LD] fp32
-  static constexpr int ML = MERGE + kWarps * 8 * LD * 4;                   // [2][warp][8 NT] fp32
-  static constexpr int PRE = ML + 2 * kWarps * 8 * NT * 4;                 // [257] units before each chunk of sequences
-  static constexpr int BAR = PRE + 272 * 4;
-  static constexpr int BYTES = BAR + kWarps * kStages * 8 + 16;
+  static constexpr int MERGE = RING + kWarps * STAGES * Unit<DH>::BYTES;  // whole items: [warp][8][LD] fp32
+  static constexpr int ML = MERGE + kWarps * 8 * LD * 4;                  // [2][warp][8 NT] fp32
+  static constexpr int PRE = MERGE;          // dealt stretches: [257] units before each run of sequences
+  static constexpr int LEN = PRE + 272 * 4;  // [256] lengths, when a run is one sequence
+  static constexpr int BAR = WHOLE ? ML + 2 * kWarps * 8 * NT * 4 : LEN + 256 * 4;
+  static constexpr int BYTES = BAR + kWarps * STAGES * 8 + 16;
 };
 
-template <int DH, typename T, int NT, int MINB>
+template <int DH, typename T, int NT, bool WHOLE, int MINB>
 __global__ void __launch_bounds__(32 * kWarps, MINB) cache_attn_kernel(const DecodeArgs a) {
   using U = Unit<DH>;
-  using S = DecodeSmem<DH, NT>;
+  using S = DecodeSmem<DH, NT, WHOLE>;
+  constexpr int kStages = S::STAGES;
   constexpr bool SPLIT = std::is_same_v<T, float>;  // two f16 terms per query and weight
   constexpr int TERMS = SPLIT ? 2 : 1;
   constexpr int KS = DH / 16, WK = DH / 32;  // k16 steps of a key, 32-bit words of it per lane
   constexpr int MT = U::TOK / 16;            // 16-key tiles of a unit
   constexpr int MU = DH / 16;                // 16-channel tiles
   extern __shared__ __align__(128) unsigned char smem[];
-  float* const merge = reinterpret_cast<float*>(smem + S::MERGE);
-  float* const ml = reinterpret_cast<float*>(smem + S::ML);
-  int* const pre = reinterpret_cast<int*>(smem + S::PRE);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + S::BAR + kWarps * kStages * 8);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   unsigned char* const ring = smem + S::RING + warp * kStages * U::BYTES;
   const uint32_t ring_s = sm100::smem_u32(ring);
   const uint32_t bars = sm100::smem_u32(smem + S::BAR) + warp * kStages * 8;
+  const int n = a.c.n_seqs, per_seq = a.c.Hkv * a.tiles;
 
   pdl_trigger();
   if (lane == 0)
     for (int i = 0; i < kStages; ++i) sm100::mbar_init(bars + 8 * i, 1);
   if (threadIdx.x == 0) *abort_flag = 0;
   sm100::fence_barrier_init();
+  __syncthreads();
   pdl_wait();  // lengths, table, pages and q come from earlier kernels of the stream
 
-  // units before each sequence: every thread counts a run of sequences, then a scan over the threads
-  const int n = a.c.n_seqs, run = (n + 32 * kWarps - 1) / (32 * kWarps);
-  const int per_seq = a.c.Hkv * a.tiles;
-  int units;
-  {
+  // ---- which units: r0 .. r1 of the list, or (WHOLE) items blockIdx.x, + gridDim.x, ..
+  int r0 = 0, r1 = 0, wid = 0;
+  const int run = (n + 32 * kWarps - 1) / (32 * kWarps);
+  int* const pre = reinterpret_cast<int*>(smem + S::PRE);
+  int* const len_s = reinterpret_cast<int*>(smem + S::LEN);
+  if constexpr (!WHOLE) {
+    // units before each sequence: every thread counts a run of sequences, then a scan over the threads
     int mine = 0;
     const int b0 = min(n, static_cast<int>(threadIdx.x) * run), b1 = min(n, b0 + run);
     for (int b = b0; b < b1; ++b) {
-      mine += span_of<U::TOK>(a.span, b).n * per_seq;
-      if (blockIdx.x == 0 && a.c.err && __ldg(a.c.lens + b) > a.span.cap) atomicOr(a.c.err, kErrPage);
+      const int len = __ldg(a.c.lens + b);
+      mine += span_of<U::TOK>(a.span, len).n * per_seq;
+      if (run == 1) len_s[b] = len;
+      if (blockIdx.x == 0 && a.c.err && len > a.span.cap) atomicOr(a.c.err, kErrPage);
     }
     int sum = mine;
 #pragma unroll
@@ -215,101 +239,102 @@ __global__ void __launch_bounds__(32 * kWarps, MINB) cache_attn_kernel(const Dec
       int at = before + sum - mine;
       for (int b = b0; b < b1; ++b) {
         a.prefix[b] = at;
-        at += span_of<U::TOK>(a.span, b).n * per_seq;
+        at += span_of<U::TOK>(a.span, __ldg(a.c.lens + b)).n * per_seq;
       }
       if (threadIdx.x == 32 * kWarps - 1) a.prefix[n] = before + sum;
     }
     __syncthreads();
-    units = pre[256];
+    const Deal d(pre[256], gridDim.x);
+    wid = warp * gridDim.x + blockIdx.x;  // a short list is spread over the SMs first
+    if (wid >= d.warps) return;
+    r0 = d.begin(wid);
+    r1 = d.begin(wid + 1);
   }
-  // this CTA's share: at least a unit per warp, the CTAs past that have none
-  const int ctas = min(static_cast<int>(gridDim.x), (units + kWarps - 1) / kWarps);
-  if (static_cast<int>(blockIdx.x) >= ctas) return;
-  const int r0 = static_cast<int>(static_cast<long long>(units) * blockIdx.x / ctas);
-  const int r1 = static_cast<int>(static_cast<long long>(units) * (blockIdx.x + 1) / ctas);
 
-  auto stretch_at = [&](int u) {
-    int lo = 0, hi = 255;  // the last run of sequences that begins at or before u and is not empty
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (pre[mid] <= u)
-        lo = mid;
-      else
-        hi = mid - 1;
+  auto item_at = [&](int u) {
+    Item x;
+    if constexpr (WHOLE) {
+      x.b = u / per_seq;
+      const int i = u - x.b * per_seq;
+      x.head = i / a.tiles;
+      x.tile = i - x.head * a.tiles;
+      x.len = __ldg(a.c.lens + x.b);
+      x.begin = 0;
+      x.s = span_of<U::TOK>(a.span, x.len);
+    } else {
+      int lo = 0, hi = 255;  // the last run of sequences that begins at or before u
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (pre[mid] <= u)
+          lo = mid;
+        else
+          hi = mid - 1;
+      }
+      int b = lo * run, at = pre[lo];
+      x.len = run == 1 ? len_s[b] : __ldg(a.c.lens + b);
+      x.s = span_of<U::TOK>(a.span, x.len);
+      while (at + x.s.n * per_seq <= u) {
+        at += x.s.n * per_seq;
+        x.len = __ldg(a.c.lens + ++b);
+        x.s = span_of<U::TOK>(a.span, x.len);
+      }
+      const int i = (u - at) / x.s.n;
+      x.b = b;
+      x.head = i / a.tiles;
+      x.tile = i - x.head * a.tiles;
+      x.begin = at + i * x.s.n;
     }
-    Stretch x;
-    int b = lo * run, at = pre[lo];
-    x.s = span_of<U::TOK>(a.span, b);
-    while (at + x.s.n * per_seq <= u) {
-      at += x.s.n * per_seq;
-      x.s = span_of<U::TOK>(a.span, ++b);
-    }
-    const int item = (u - at) / x.s.n;
-    x.b = b;
-    x.head = item / a.tiles;
-    x.tile = item - x.head * a.tiles;
-    x.begin = at + item * x.s.n;
-    x.end = x.begin + x.s.n;
     return x;
   };
-  auto first_token = [&](const Stretch& x, int u) {
-    const int k = u - x.begin;
-    return (k < x.s.sinks ? k : x.s.lo + k - x.s.sinks) * U::TOK;
-  };
-
-  // ---- this warp's copies, running kStages units ahead; a page id is looked up one unit earlier still
-  Stretch px = stretch_at(r0);
-  int pu = r0 + warp, page_next = 0, tok_next = 0;
-  bool more = true;
-  unsigned bad = 0;  // bit per stage: no such page, the unit's keys are masked
-  auto look_up = [&]() {  // finds the page of unit pu
-    if (pu >= r1) {
-      more = false;
-      return;
-    }
-    if (pu >= px.end) px = stretch_at(pu);
-    tok_next = first_token(px, pu);
-    page_next = __ldg(a.c.table + static_cast<size_t>(px.b) * a.c.max_pages + tok_next / kPage);
-  };
-  auto copy = [&](int st) {  // issues the unit that look_up found, then looks up the next
-    if (!more) return;
-    int page = page_next;
-    bad &= ~(1u << st);
-    if (page < 0 || page >= a.c.n_pages) {
-      if (lane == 0 && a.c.err) atomicOr(a.c.err, kErrPage);
-      bad |= 1u << st;
-      page = 0;
-    }
-    if (lane == 0) {
-      const unsigned char* src = a.c.pages + cache4::block_offset<DH>(a.c, page, px.head);
-      const uint32_t dst = ring_s + st * U::BYTES, bar = bars + 8 * st;
-      sm100::mbar_arrive_expect_tx(bar, U::BYTES);
-      if constexpr (U::TOK == kPage) {
-        sm100::bulk_load(dst, src, U::BYTES, bar);
-      } else {
-        using L = cache4::Layout<DH>;
-        const int r = tok_next % kPage;
-#pragma unroll
-        for (int v = 0; v < 2; ++v) {
-          sm100::bulk_load(dst + v * U::V_OFF, src + v * L::V_OFF + r * L::CODE_ROW, U::CODES, bar);
-          sm100::bulk_load(dst + v * U::V_OFF + U::CODES, src + v * L::V_OFF + L::CODES + r * L::SCALE_ROW, U::SCALES,
-                           bar);
-        }
-      }
-    }
-    pu += kWarps;
-    look_up();
-  };
-  look_up();
-  int issued = 0, used = 0;
-  for (; issued < kStages && more; ++issued) copy(issued);
+  auto first_token = [&](const Item& x, int k) { return (k < x.s.sinks ? k : x.s.lo + k - x.s.sinks) * U::TOK; };
 
   bool dead = false;
-  int u = r0 + warp;  // this warp's units: every eighth of the share
-  for (int u0 = r0; u0 < r1;) {
-    const Stretch x = stretch_at(u0);
-    const int u1 = min(x.end, r1);
-    const int len = __ldg(a.c.lens + x.b), first_pos = len - a.n_q;
+  int issued = 0, used = 0;  // units copied and consumed by this warp (ring stages)
+  unsigned bad = 0;          // bit per stage: no such page, the unit's keys are masked
+  const int items = n * per_seq;
+  for (int at = WHOLE ? static_cast<int>(blockIdx.x) : r0; at < (WHOLE ? items : r1);) {
+    const Item x = item_at(at);
+    // this warp's units of the item: k0, k0 + step, .. (count of them)
+    const int step = WHOLE ? kWarps : 1;
+    const int k0 = WHOLE ? warp : at - x.begin;
+    const int k1 = WHOLE ? x.s.n : min(x.s.n, r1 - x.begin);
+    const int count = max(0, (k1 - k0 + step - 1) / step);
+    if (WHOLE && x.head == 0 && x.tile == 0 && threadIdx.x == 0 && a.c.err && x.len > a.span.cap)
+      atomicOr(a.c.err, kErrPage);
+    int pages = 0;  // of units 32 j .. 32 j + 31, one per lane
+    auto copy = [&](int i) {
+      if ((i & 31) == 0 && i + lane < count)
+        pages = __ldg(a.c.table + static_cast<size_t>(x.b) * a.c.max_pages +
+                      first_token(x, k0 + (i + lane) * step) / kPage);
+      int page = __shfl_sync(0xffffffffu, pages, i & 31);
+      const int st = issued % kStages;
+      ++issued;
+      bad &= ~(1u << st);
+      if (page < 0 || page >= a.c.n_pages) {
+        if (lane == 0 && a.c.err) atomicOr(a.c.err, kErrPage);
+        bad |= 1u << st;
+        page = 0;
+      }
+      if (lane == 0) {
+        const unsigned char* src = a.c.pages + cache4::block_offset<DH>(a.c, page, x.head);
+        const uint32_t dst = ring_s + st * U::BYTES, bar = bars + 8 * st;
+        sm100::mbar_arrive_expect_tx(bar, U::BYTES);
+        if constexpr (U::TOK == kPage) {
+          sm100::bulk_load(dst, src, U::BYTES, bar);
+        } else {
+          using L = cache4::Layout<DH>;
+          const int r = first_token(x, k0 + i * step) % kPage;
+#pragma unroll
+          for (int v = 0; v < 2; ++v) {
+            sm100::bulk_load(dst + v * U::V_OFF, src + v * L::V_OFF + r * L::CODE_ROW, U::CODES, bar);
+            sm100::bulk_load(dst + v * U::V_OFF + U::CODES, src + v * L::V_OFF + L::CODES + r * L::SCALE_ROW,
+                             U::SCALES, bar);
+          }
+        }
+      }
+    };
+    for (int i = 0; i < min(kStages, count); ++i) copy(i);
+    const int len = x.len, first_pos = len - a.n_q;
 
     // ---- the tile's queries: row n of tile j, channels of this lane's share of a key
     uint32_t q[NT][TERMS][KS][2];
@@ -360,6 +385,7 @@ __global__ void __launch_bounds__(32 * kWarps, MINB) cache_attn_kernel(const Dec
           q[j][0][2 * w + (i >> 1)][i & 1] = pack2<__half>(v0, v1);
           if constexpr (SPLIT) q[j][1][2 * w + (i >> 1)][i & 1] = pack2<__half>(lo_term<__half>(v0), lo_term<__half>(v1));
         }
+      fin |= first_pos + tok < 0;  // a row that sees nothing gives zeros whatever it holds
       const float scale = fin ? down * (kCodeScale * rsqrtf(static_cast<float>(DH)) * 1.4426950408889634f) : NAN;
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
@@ -377,9 +403,9 @@ __global__ void __launch_bounds__(32 * kWarps, MINB) cache_attn_kernel(const Dec
       for (int i = 0; i < MU; ++i) o[j][i][0] = o[j][i][1] = o[j][i][2] = o[j][i][3] = 0.f;
     }
 
-    for (; u < u1; u += kWarps) {
+    for (int i = 0; i < count; ++i) {
       const int st = used % kStages;
-      const int key0 = first_token(x, u);
+      const int key0 = first_token(x, k0 + i * step);
       const bool gone = (bad >> st) & 1u;
       const unsigned char* const kc = ring + st * U::BYTES;
       if (!sm100::mbar_wait(bars + 8 * st, (used / kStages) & 1, abort_flag)) dead = true;
@@ -518,13 +544,8 @@ __global__ void __launch_bounds__(32 * kWarps, MINB) cache_attn_kernel(const Dec
       }
       __syncwarp();  // every lane has read the stage
       ++used;
-      if (more) {
-        copy(st);
-        ++issued;
-      }
+      if (i + kStages < count) copy(i + kStages);
     }
-
-    // ---- the warps' results of this stretch, added
 #pragma unroll
     for (int j = 0; j < NT; ++j)
 #pragma unroll
@@ -533,157 +554,231 @@ __global__ void __launch_bounds__(32 * kWarps, MINB) cache_attn_kernel(const Dec
         l[j][c] += __shfl_xor_sync(0xffffffffu, l[j][c], 8);
         l[j][c] += __shfl_xor_sync(0xffffffffu, l[j][c], 16);
         m[j][c] *= rs[j][c];  // in powers of 2
-        if (g == 0) {
-          ml[warp * 8 * NT + 8 * j + 2 * t + c] = m[j][c];
-          ml[(kWarps + warp) * 8 * NT + 8 * j + 2 * t + c] = l[j][c];
-        }
       }
-    const bool whole = u0 == x.begin && u1 == x.end;
-    float* const part = a.parts + static_cast<size_t>(2 * blockIdx.x + (u0 == r0 ? 0 : 1)) * (DH + 2) * 8 * NT;
+    auto out_row = [&](int rr) {
+      const int tok = rr / a.group, hd = rr - tok * a.group;
+      return static_cast<T*>(a.out) + ((static_cast<size_t>(x.b) * a.n_q + tok) * a.H + x.head * a.group + hd) * DH;
+    };
+    if constexpr (WHOLE) {
+      // the warps' results of the item, added
+      float* const merge = reinterpret_cast<float*>(smem + S::MERGE);
+      float* const ml = reinterpret_cast<float*>(smem + S::ML);
 #pragma unroll
-    for (int j = 0; j < NT; ++j) {
-      __syncthreads();
+      for (int j = 0; j < NT; ++j)
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        float top = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, ml[w * 8 * NT + 8 * j + 2 * t + c]);
-        const float by = top == -INFINITY && m[j][c] == top ? (l[j][c] == l[j][c] ? 0.f : NAN) : ex2(m[j][c] - top);
-#pragma unroll
-        for (int i = 0; i < MU; ++i)
-          *reinterpret_cast<float2*>(merge + (warp * 8 + 2 * t + c) * S::LD + g * (DH / 8) + 2 * i) =
-              make_float2(o[j][i][c] * by, o[j][i][c + 2] * by);
-      }
-      __syncthreads();
-      for (int e = threadIdx.x; e < 8 * DH / 4; e += 32 * kWarps) {
-        const int row = e / (DH / 4), ch = (e - row * (DH / 4)) * 4;
-        float top = -INFINITY, sum = 0.f;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, ml[w * 8 * NT + 8 * j + row]);
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          const float lw = ml[(kWarps + w) * 8 * NT + 8 * j + row], mw = ml[w * 8 * NT + 8 * j + row];
-          sum += mw == -INFINITY ? lw * 0.f : lw * ex2(mw - top);  // 0, or NaN of a query that is not finite
-          const float4 v = *reinterpret_cast<const float4*>(merge + (w * 8 + row) * S::LD + ch);
-          acc.x += v.x, acc.y += v.y, acc.z += v.z, acc.w += v.w;
-        }
-        const int rr = (x.tile * NT + j) * 8 + row;
-        if (whole) {
-          if (rr < a.rows) {
-            const int tok = rr / a.group, hd = rr - tok * a.group;
-            T* dst = static_cast<T*>(a.out) +
-                     ((static_cast<size_t>(x.b) * a.n_q + tok) * a.H + x.head * a.group + hd) * DH + ch;
-            const float inv = sum == 0.f ? 0.f : kCodeScale / sum;
-            if constexpr (SPLIT)
-              *reinterpret_cast<float4*>(dst) = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-            else
-              *reinterpret_cast<uint2*>(dst) =
-                  make_uint2(pack2<T>(acc.x * inv, acc.y * inv), pack2<T>(acc.z * inv, acc.w * inv));
+        for (int c = 0; c < 2; ++c)
+          if (g == 0) {
+            ml[warp * 8 * NT + 8 * j + 2 * t + c] = m[j][c];
+            ml[(kWarps + warp) * 8 * NT + 8 * j + 2 * t + c] = l[j][c];
           }
-        } else {
-          *reinterpret_cast<float4*>(part + (8 * j + row) * DH + ch) = acc;
-          if (ch == 0) {
-            part[8 * NT * DH + 8 * j + row] = top;
-            part[8 * NT * (DH + 1) + 8 * j + row] = sum;
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        __syncthreads();
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          float top = -INFINITY;
+#pragma unroll
+          for (int w = 0; w < kWarps; ++w) top = fmaxf(top, ml[w * 8 * NT + 8 * j + 2 * t + c]);
+          const float by = top == -INFINITY && m[j][c] == top ? (l[j][c] == l[j][c] ? 0.f : NAN) : ex2(m[j][c] - top);
+#pragma unroll
+          for (int i = 0; i < MU; ++i)
+            *reinterpret_cast<float2*>(merge + (warp * 8 + 2 * t + c) * S::LD + g * (DH / 8) + 2 * i) =
+                make_float2(o[j][i][c] * by, o[j][i][c + 2] * by);
+        }
+        __syncthreads();
+        for (int e = threadIdx.x; e < 8 * DH / 4; e += 32 * kWarps) {
+          const int row = e / (DH / 4), ch = (e - row * (DH / 4)) * 4;
+          const int rr = (x.tile * NT + j) * 8 + row;
+          if (rr >= a.rows) continue;
+          float top = -INFINITY, sum = 0.f;
+#pragma unroll
+          for (int w = 0; w < kWarps; ++w) top = fmaxf(top, ml[w * 8 * NT + 8 * j + row]);
+          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int w = 0; w < kWarps; ++w) {
+            const float lw = ml[(kWarps + w) * 8 * NT + 8 * j + row], mw = ml[w * 8 * NT + 8 * j + row];
+            sum += mw == -INFINITY ? lw * 0.f : lw * ex2(mw - top);  // 0, or NaN of a query that is not finite
+            const float4 v = *reinterpret_cast<const float4*>(merge + (w * 8 + row) * S::LD + ch);
+            acc.x += v.x, acc.y += v.y, acc.z += v.z, acc.w += v.w;
           }
+          T* dst = out_row(rr) + ch;
+          const float inv = sum == 0.f ? 0.f : kCodeScale / sum;
+          if constexpr (SPLIT)
+            *reinterpret_cast<float4*>(dst) = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+          else
+            *reinterpret_cast<uint2*>(dst) =
+                make_uint2(pack2<T>(acc.x * inv, acc.y * inv), pack2<T>(acc.z * inv, acc.w * inv));
         }
       }
+      __syncthreads();  // ml and merge may be written again
+      at += gridDim.x;
+    } else {
+      const bool all = k0 == 0 && k1 == x.s.n;
+      float* const part = a.parts + static_cast<size_t>(2 * wid + (at == r0 ? 0 : 1)) * (DH + 2) * 8 * NT;
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const int row = 8 * j + 2 * t + c, rr = x.tile * NT * 8 + row;
+          if (rr >= a.rows) continue;
+          if (all) {
+            T* dst = out_row(rr) + g * (DH / 8);
+            const float inv = l[j][c] == 0.f ? 0.f : kCodeScale / l[j][c];
+#pragma unroll
+            for (int i = 0; i < MU; ++i) {
+              const float v0 = o[j][i][c] * inv, v1 = o[j][i][c + 2] * inv;
+              if constexpr (SPLIT)
+                *reinterpret_cast<float2*>(dst + 2 * i) = make_float2(v0, v1);
+              else
+                *reinterpret_cast<uint32_t*>(dst + 2 * i) = pack2<T>(v0, v1);
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < MU; ++i)
+              *reinterpret_cast<float2*>(part + row * DH + g * (DH / 8) + 2 * i) =
+                  make_float2(o[j][i][c], o[j][i][c + 2]);
+            if (g == 0) {
+              part[8 * NT * DH + row] = m[j][c];
+              part[8 * NT * (DH + 1) + row] = l[j][c];
+            }
+          }
+        }
+      at = x.begin + k1;
     }
-    __syncthreads();  // ml and merge may be written again
-    u0 = u1;
   }
   if (dead) {
     if (lane == 0 && a.c.err) atomicOr(a.c.err, kErrTimeoutEpilogue);
-    for (int k = max(used - kStages, 0); k < issued; ++k) sm100::mbar_wait_drain(bars + 8 * (k % kStages), (k / kStages) & 1);
+    for (int k = max(used - kStages, 0); k < issued; ++k)
+      sm100::mbar_wait_drain(bars + 8 * (k % kStages), (k / kStages) & 1);
   }
 }
 
-// Rows of items that several CTAs shared: their parts added in the order of the keys. Rows that
-// see nothing: zeros. One CTA per (sequence, kv head, row tile), one warp per row.
+// Rows of items that several warps shared: their parts added in the order of the keys. Rows that
+// see nothing: zeros. One CTA per row; its eight warps take a range of the parts each.
 template <int DH, typename T, int NT>
-__global__ void __launch_bounds__(32 * 8 * NT) cache_attn_join_kernel(const DecodeArgs a, int max_ctas) {
+__global__ void __launch_bounds__(256) cache_attn_join_kernel(const DecodeArgs a, int ctas) {
   pdl_trigger();
   pdl_wait();
-  const int tile = blockIdx.x % a.tiles, head = (blockIdx.x / a.tiles) % a.c.Hkv, b = blockIdx.x / (a.tiles * a.c.Hkv);
-  const int units = a.prefix[a.c.n_seqs], at = a.prefix[b];
+  constexpr int C = DH / 32, JW = 8;
+  __shared__ float sums[JW], sacc[JW][DH], stop[JW];
+  const int rows = a.rows, per_seq = a.c.Hkv * rows;
+  const int b = blockIdx.x / per_seq, hr = blockIdx.x - b * per_seq;
+  const int head = hr / rows, rr = hr - head * rows;
+  const int tile = rr / (8 * NT), row = rr - tile * 8 * NT;
+  const int at = a.prefix[b], units = a.prefix[a.c.n_seqs];
   const int n = (a.prefix[b + 1] - at) / (a.c.Hkv * a.tiles);
-  const int row = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rr = tile * 8 * NT + row;
-  if (rr >= a.rows) return;
-  const int tok = rr / a.group, hd = rr - tok * a.group;
-  T* dst = static_cast<T*>(a.out) + ((static_cast<size_t>(b) * a.n_q + tok) * a.H + head * a.group + hd) * DH;
-  constexpr int C = DH / 32;
-  float acc[C];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const Deal d(units, ctas);
+  const int begin = at + (head * a.tiles + tile) * n;
+  int w0 = 0, w1 = -1;
+  if (n > 0) {
+    w0 = d.warp_of(begin);
+    w1 = d.warp_of(begin + n - 1);
+    if (w0 == w1) return;  // that warp wrote the result
+  }
+  auto part_of = [&](int w) {
+    const int first = d.begin(w);
+    return a.parts + static_cast<size_t>(2 * w + (begin <= first ? 0 : 1)) * (DH + 2) * 8 * NT;
+  };
+  const int each = (w1 - w0 + JW) / JW, from = w0 + warp * each, to = min(from + each, w1 + 1);
+  float acc[C], sum = 0.f, top = -INFINITY;
 #pragma unroll
   for (int i = 0; i < C; ++i) acc[i] = 0.f;
-  float sum = 0.f;
-  if (n > 0) {
-    const int begin = at + (head * a.tiles + tile) * n, end = begin + n;
-    const int ctas = min(max_ctas, (units + kWarps - 1) / kWarps);
-    auto cta_of = [&](int u) {
-      return static_cast<int>((static_cast<long long>(u + 1) * ctas - 1) / units);
-    };
-    const int w0 = cta_of(begin), w1 = cta_of(end - 1);
-    if (w0 == w1) return;  // that CTA wrote the result
-    auto part_of = [&](int w) {
-      const int r0 = static_cast<int>(static_cast<long long>(units) * w / ctas);
-      return a.parts + static_cast<size_t>(2 * w + (max(begin, r0) == r0 ? 0 : 1)) * (DH + 2) * 8 * NT;
-    };
-    float top = -INFINITY;
-    for (int w = w0 + lane; w <= w1; w += 32) top = fmaxf(top, part_of(w)[8 * NT * DH + row]);
+  for (int w = from; w < to; w += 32) {
+    // 32 parts at a time: a lane's own maximum and sum, then every part's output
+    const bool on = w + lane < to;
+    const float* p = part_of(on ? w + lane : w);
+    const float mw = on ? p[8 * NT * DH + row] : -INFINITY, lw = on ? p[8 * NT * (DH + 1) + row] : 0.f;
+    float mx = mw;
 #pragma unroll
-    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    for (int w = w0; w <= w1; ++w) {
-      const float* p = part_of(w);
-      const float mw = p[8 * NT * DH + row], lw = p[8 * NT * (DH + 1) + row];
-      const float by = mw == -INFINITY ? 0.f : ex2(mw - top);
-      sum += lw * by;
+    for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    const float up = fmaxf(top, mx);
+    const float keep = top == -INFINITY ? 0.f : ex2(top - up), by = mw == -INFINITY ? 0.f : ex2(mw - up);
+    top = up;
+    sum *= keep;
 #pragma unroll
-      for (int i = 0; i < C; ++i) acc[i] = fmaf(p[row * DH + 32 * i + lane], by, acc[i]);
+    for (int i = 0; i < C; ++i) acc[i] *= keep;
+    const int many = min(32, to - w);
+#pragma unroll 4
+    for (int k = 0; k < many; ++k) {
+      const float f = __shfl_sync(0xffffffffu, by, k);
+      sum = fmaf(__shfl_sync(0xffffffffu, lw, k), f, sum);
+      const float* q = part_of(w + k) + row * DH + lane;
+#pragma unroll
+      for (int i = 0; i < C; ++i) acc[i] = fmaf(q[32 * i], f, acc[i]);
     }
   }
-  const float inv = sum == 0.f ? 0.f : kCodeScale / sum;
+  if (lane == 0) {
+    sums[warp] = sum;
+    stop[warp] = top;
+  }
 #pragma unroll
-  for (int i = 0; i < C; ++i) dst[32 * i + lane] = from_f32<T>(acc[i] * inv);
+  for (int i = 0; i < C; ++i) sacc[warp][32 * i + lane] = acc[i];
+  __syncthreads();
+  if (threadIdx.x < DH) {
+    float tt = -INFINITY, ss = 0.f, v = 0.f;
+#pragma unroll
+    for (int w = 0; w < JW; ++w) tt = fmaxf(tt, stop[w]);
+#pragma unroll
+    for (int w = 0; w < JW; ++w) {
+      const float f = stop[w] == -INFINITY ? 0.f : ex2(stop[w] - tt);
+      ss = fmaf(sums[w], f, ss);
+      v = fmaf(sacc[w][threadIdx.x], f, v);
+    }
+    const int tok = rr / a.group, hd = rr - tok * a.group;
+    static_cast<T*>(a.out)[((static_cast<size_t>(b) * a.n_q + tok) * a.H + head * a.group + hd) * DH + threadIdx.x] =
+        from_f32<T>(ss == 0.f ? 0.f : v * (kCodeScale / ss));
+  }
 }
 
 int tile_rows(int rows, bool bf16) { return bf16 && rows > 8 ? 16 : 8; }
 
-// Most units a call may have, and the CTAs for them
-long long most_units(int n_seqs, int max_pages, int n_q, int tiles, int Hkv, int dh, int window, int sinks) {
+// Most units an item may have, and what follows from it
+long long most_units(int max_pages, int n_q, int dh, int window, int sinks) {
   const int tok = dh == 128 ? 32 : 64;
   const long long all = static_cast<long long>(max_pages) * kPage / tok;
   // a window and the tokens before it cross at most one more unit than they fill
   const long long seen = (static_cast<long long>(window) + n_q + tok - 2) / tok + 1 + (sinks + tok - 1LL) / tok;
-  return static_cast<long long>(n_seqs) * Hkv * tiles * (all < seen ? all : seen);
+  return all < seen ? all : seen;
 }
-int cta_count(long long units) {
-  const long long c = (units + kWarps - 1) / kWarps;
-  return static_cast<int>(c < kMaxCtas ? c : kMaxCtas);
+struct Plan {
+  bool whole;
+  long long items, units;
+  int ctas;
+};
+Plan plan_of(int n_seqs, int max_pages, int n_q, int tiles, int Hkv, int dh, int window, int sinks) {
+  Plan p;
+  const long long most = most_units(max_pages, n_q, dh, window, sinks);
+  p.items = static_cast<long long>(n_seqs) * Hkv * tiles;
+  p.units = p.items * most;
+  p.whole = most <= kWholeUnits;
+  const long long want = p.whole ? p.items : (p.units + kWarps * kLeastUnits - 1) / (kWarps * kLeastUnits);
+  p.ctas = static_cast<int>(want < kMaxCtas ? want : kMaxCtas);
+  return p;
 }
 
 template <int DH, typename T, int NT>
 cudaError_t launch_decode(const CacheAttnArgs& c, cudaStream_t st) {
-  using S = DecodeSmem<DH, NT>;
   constexpr int MINB = DH == 128 && NT == 2 ? 1 : 2;
   DecodeArgs a{};
   a.c = c.c;
-  a.span = {c.c.lens, c.c.max_pages * kPage, c.n_q, c.window, c.sinks};
+  a.span = {c.c.max_pages * kPage, c.n_q, c.window, c.sinks};
   a.q = c.q, a.ldq = c.ldq, a.out = c.out;
   a.n_q = c.n_q, a.H = c.H, a.group = c.H / c.c.Hkv;
   a.rows = c.n_q * a.group;
   a.tiles = (a.rows + 8 * NT - 1) / (8 * NT);
-  const int ctas = cta_count(most_units(c.c.n_seqs, c.c.max_pages, c.n_q, a.tiles, c.c.Hkv, DH, c.window, c.sinks));
-  a.parts = static_cast<float*>(c.ws);
-  a.prefix = reinterpret_cast<int*>(a.parts + static_cast<size_t>(2) * ctas * (DH + 2) * 8 * NT);
-  auto kernel = cache_attn_kernel<DH, T, NT, MINB>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::BYTES);
+  const Plan p = plan_of(c.c.n_seqs, c.c.max_pages, c.n_q, a.tiles, c.c.Hkv, DH, c.window, c.sinks);
+  auto kernel = p.whole ? cache_attn_kernel<DH, T, NT, true, MINB> : cache_attn_kernel<DH, T, NT, false, MINB>;
+  const int smem = p.whole ? DecodeSmem<DH, NT, true>::BYTES : DecodeSmem<DH, NT, false>::BYTES;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(kernel, dim3(ctas), dim3(32 * kWarps), S::BYTES, st, a);
-  if (e != cudaSuccess) return e;
-  e = launch_pdl(cache_attn_join_kernel<DH, T, NT>, dim3(c.c.n_seqs * c.c.Hkv * a.tiles), dim3(32 * 8 * NT), 0, st, a,
-                 ctas);
+  if (!p.whole) {
+    a.parts = static_cast<float*>(c.ws);
+    a.prefix = reinterpret_cast<int*>(a.parts + static_cast<size_t>(2 * kWarps) * p.ctas * (DH + 2) * 8 * NT);
+  }
+  e = launch_pdl(kernel, dim3(p.ctas), dim3(32 * kWarps), smem, st, a);
+  if (e == cudaSuccess && !p.whole)
+    e = launch_pdl(cache_attn_join_kernel<DH, T, NT>, dim3(c.c.n_seqs * c.c.Hkv * a.rows), dim3(256), 0, st, a, p.ctas);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
@@ -702,9 +797,9 @@ size_t cache_attention_workspace(int n_seqs, int max_pages, int n_q, int H, int 
   const int rows = n_q * (H / Hkv);
   for (int bf16 = 0; bf16 < 2; ++bf16) {
     const int tr = tile_rows(rows, bf16), tiles = (rows + tr - 1) / tr;
-    const long long units = most_units(n_seqs, max_pages, n_q, tiles, Hkv, dh, window, sinks);
-    if (units > 0x7fffffffLL) return 0;
-    const size_t bytes = static_cast<size_t>(2) * cta_count(units) * (dh + 2) * tr * 4;
+    const Plan p = plan_of(n_seqs, max_pages, n_q, tiles, Hkv, dh, window, sinks);
+    if (p.units > 0x7fffffffLL) return 0;
+    const size_t bytes = p.whole ? 0 : static_cast<size_t>(2 * kWarps) * p.ctas * (dh + 2) * tr * 4;
     most = bytes > most ? bytes : most;
   }
   return most + (static_cast<size_t>(n_seqs) + 1) * 4;

@@ -311,6 +311,37 @@ def test_cache_attention_of_queries_that_are_not_finite(cuda_ok):
 
 
 @gpu
+@pytest.mark.parametrize("n_q,window", [(1, 0), (2, 100)])
+def test_rows_of_unused_slots_give_zeros_whatever_they_hold(cuda_ok, n_q, window):
+    s = Setup([0, 3000, 1], 1, 64)
+    s.fill(1)
+    q = normal(2, (3, n_q, 4 * 64), "bf16")
+    want = s.attend(q, n_q, 4, window, 0, "bf16")
+    q[0] = float("nan")
+    q[2, :n_q - 1] = float("inf")
+    got = s.attend(q, n_q, 4, window, 0, "bf16")
+    rmt.rmt_sync(None)
+    assert torch.equal(got, want) and not got[0].any() and not got[2, :n_q - 1].any()
+
+
+@gpu
+@pytest.mark.parametrize("n", [255, 256, 257, 700])
+def test_many_sequences(cuda_ok, n):
+    """More sequences than a CTA has threads, lengths from 0 to 2500: each result is the one-sequence call's."""
+    lens = [(i * 37) % 90 if i % 50 else 2500 - i for i in range(n)]
+    s = Setup(lens, 1, 64)
+    s.fill(3, "bf16")
+    q = normal(4, (n, 1, 2 * 64), "bf16")
+    got = f64(s.attend(q, 1, 2, 0, 0, "bf16"))
+    rmt.rmt_sync(None)
+    vals = s.values()
+    for b in list(range(0, n, 7)) + list(range(0, n, 50)) + [n - 1]:
+        k, v = vals[b]
+        ref = attend_ref(f64(q)[b].reshape(1, 2, 64), k, v, np.array([lens[b] - 1]), 0, 0)
+        check_attention(got[b].reshape(1, 2, 64), ref, np.abs(v).max() if v.size else 0.0, "bf16")
+
+
+@gpu
 def test_cache_offsets_past_32_bits(cuda_ok):
     dh, Hkv, H = 128, 8, 16
     page = rmt.rmt_cache_page_bytes(Hkv, dh)
