@@ -24,8 +24,8 @@
 // Q has the same one, and for V eight neighbouring lanes' keys are chosen so that the reads of a warp are
 // whole lines of shared memory. P^T turns from accumulator to operand layout by
 // movmatrix. Queries are scaled by a power of two per row into f16's normal range: exact for
-// bf16; fp32 queries and weights are taken as two f16 terms (22 bits). Weights are held at 2^15 of
-// their value (at most 32768): what f16 cuts off is below 2^-40 of the largest.
+// bf16; fp32 queries and weights are taken as two f16 terms (22 bits). Weights are held at 2^7 to 2^15
+// of their value: what f16 cuts off is below 2^-31 of the largest.
 #include "cache4.cuh"
 #include "launch.h"
 #include "sm100.cuh"
@@ -36,8 +36,7 @@ namespace {
 using cache4::CacheArgs;
 using cache4::kPage;
 
-constexpr int kWarps = 8;
-constexpr int kMaxCtas = 296;    // two per SM
+constexpr int kMaxWarps = 148 * 16;  // that share a list of units: 16 per SM
 constexpr int kLeastUnits = 4;   // of a warp's stretch
 constexpr int kWholeUnits = 32;  // items up to this many units are not split
 constexpr float kCodeScale = 16.f;  // operands hold 2^-4 of a value
@@ -83,9 +82,9 @@ struct DecodeArgs {
 // The list of units dealt to warps: equal stretches, the first `more` of them one unit longer.
 struct Deal {
   int warps, units, each, more;
-  __device__ __forceinline__ Deal(int units_, int ctas) {
+  __device__ __forceinline__ Deal(int units_, int grid_warps) {
     units = units_;
-    warps = max(1, min(ctas * kWarps, (units + kLeastUnits - 1) / kLeastUnits));
+    warps = max(1, min(grid_warps, (units + kLeastUnits - 1) / kLeastUnits));
     each = units / warps;
     more = units - each * warps;
   }
@@ -101,11 +100,24 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+// (x, y) = (x, y) * (a, b) + (c, d)
+__device__ __forceinline__ void fma_pair(float& x, float& y, float a, float b, float c, float d) {
+  asm("{\n\t.reg .b64 p, q, r;\n\t"
+      "mov.b64 p, {%0, %1};\n\tmov.b64 q, {%2, %3};\n\tmov.b64 r, {%4, %5};\n\t"
+      "fma.rn.f32x2 p, p, q, r;\n\tmov.b64 {%0, %1}, p;\n\t}"
+      : "+f"(x), "+f"(y)
+      : "f"(a), "f"(b), "f"(c), "f"(d));
+}
 __device__ __forceinline__ uint32_t h2(__half2 v) { return *reinterpret_cast<uint32_t*>(&v); }
 __device__ __forceinline__ __half2 as_h2(uint32_t v) { return *reinterpret_cast<__half2*>(&v); }
 __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                     uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
       "{%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
@@ -113,20 +125,21 @@ __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uin
 }
 __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
   uint32_t r;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
   return r;
 }
 
-// Two scale bytes (low and high half of b) as f16 pairs: 2^-4 of the scales (x), -72 (y) and -8
+// Two scales (f16 bits in the low and high half of b) as pairs: 2^-4 of the scales (x), -72 (y) and -8
 // (z) times that.
 struct Scale {
   __half2 x, y, z;
 };
 __device__ __forceinline__ Scale scale_pair(uint32_t b) {
   Scale s;
-  s.x = __hmul2(as_h2(b << 7), __float2half2_rn(1.f / kCodeScale));
-  s.y = __hmul2(s.x, __float2half2_rn(-72.f));
-  s.z = __hmul2(s.x, __float2half2_rn(-8.f));
+  const __half2 f = as_h2(b);
+  s.x = __hmul2(f, __float2half2_rn(1.f / kCodeScale));
+  s.y = __hmul2(f, __float2half2_rn(-72.f / kCodeScale));
+  s.z = __hmul2(f, __float2half2_rn(-8.f / kCodeScale));
   return s;
 }
 __device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t b, uint32_t c) {
@@ -169,24 +182,35 @@ struct Item {
   Span s;
 };
 
+// Warps of a CTA, one CTA per SM: 16 of at most 128 registers, but where two row tiles of 128
+// channels need more: 12 of 168. (Of two CTAs with 8 warps each the first on an SM is served first:
+// it ended after 38 us of 64 sequences' 50, the other's four warps per scheduler then ran alone.)
+template <int DH, int NT>
+struct Shape {
+  static constexpr bool WIDE = DH == 128 && NT == 2;
+  static constexpr int WARPS = WIDE ? 12 : 16;
+};
+
 template <int DH, int NT, bool WHOLE>
 struct DecodeSmem {
+  static constexpr int kWarps = Shape<DH, NT>::WARPS;
   static constexpr int STAGES = WHOLE ? 2 : 3;  // of a warp's ring
   static constexpr int RING = 0;
   static constexpr int LD = DH + 4;
   static constexpr int MERGE = RING + kWarps * STAGES * Unit<DH>::BYTES;  // whole items: [warp][8][LD] fp32
   static constexpr int ML = MERGE + kWarps * 8 * LD * 4;                  // [2][warp][8 NT] fp32
-  static constexpr int PRE = MERGE;          // dealt stretches: [257] units before each run of sequences
-  static constexpr int LEN = PRE + 272 * 4;  // [256] lengths, when a run is one sequence
-  static constexpr int BAR = WHOLE ? ML + 2 * kWarps * 8 * NT * 4 : LEN + 256 * 4;
+  static constexpr int PRE = MERGE;  // dealt stretches: [threads + 1] units before each run of sequences
+  static constexpr int SUM = PRE + (32 * kWarps + 4) * 4;  // [warps]
+  static constexpr int LEN = SUM + 16 * 4;                 // [threads] lengths, when a run is one sequence
+  static constexpr int BAR = WHOLE ? ML + 2 * kWarps * 8 * NT * 4 : LEN + 32 * kWarps * 4;
   static constexpr int BYTES = BAR + kWarps * STAGES * 8 + 16;
 };
 
-template <int DH, typename T, int NT, bool WHOLE, int MINB>
-__global__ void __launch_bounds__(32 * kWarps, MINB) cache_attn_kernel(const DecodeArgs a) {
+template <int DH, typename T, int NT, bool WHOLE>
+__global__ void __launch_bounds__(32 * Shape<DH, NT>::WARPS, 1) cache_attn_kernel(const DecodeArgs a) {
   using U = Unit<DH>;
   using S = DecodeSmem<DH, NT, WHOLE>;
-  constexpr int kStages = S::STAGES;
+  constexpr int kStages = S::STAGES, kWarps = S::kWarps, kThreads = 32 * kWarps;
   constexpr bool SPLIT = std::is_same_v<T, float>;  // two f16 terms per query and weight
   constexpr int TERMS = SPLIT ? 2 : 1;
   constexpr int KS = DH / 16, WK = DH / 32;  // k16 steps of a key, 32-bit words of it per lane
@@ -210,8 +234,9 @@ __global__ void __launch_bounds__(32 * kWarps, MINB) cache_attn_kernel(const Dec
 
   // ---- which units: r0 .. r1 of the list, or (WHOLE) items blockIdx.x, + gridDim.x, ..
   int r0 = 0, r1 = 0, wid = 0;
-  const int run = (n + 32 * kWarps - 1) / (32 * kWarps);
+  const int run = (n + kThreads - 1) / kThreads;
   int* const pre = reinterpret_cast<int*>(smem + S::PRE);
+  int* const sum_s = reinterpret_cast<int*>(smem + S::SUM);
   int* const len_s = reinterpret_cast<int*>(smem + S::LEN);
   if constexpr (!WHOLE) {
     // units before each sequence: every thread counts a run of sequences, then a scan over the threads
@@ -229,22 +254,22 @@ __global__ void __launch_bounds__(32 * kWarps, MINB) cache_attn_kernel(const Dec
       const int v = __shfl_up_sync(0xffffffffu, sum, o);
       if (lane >= o) sum += v;
     }
-    if (lane == 31) pre[260 + warp] = sum;
+    if (lane == 31) sum_s[warp] = sum;
     __syncthreads();
     int before = 0;
-    for (int w = 0; w < warp; ++w) before += pre[260 + w];
+    for (int w = 0; w < warp; ++w) before += sum_s[w];
     pre[threadIdx.x] = before + sum - mine;
-    if (threadIdx.x == 32 * kWarps - 1) pre[256] = before + sum;
+    if (threadIdx.x == kThreads - 1) pre[kThreads] = before + sum;
     if (blockIdx.x == 0) {
       int at = before + sum - mine;
       for (int b = b0; b < b1; ++b) {
         a.prefix[b] = at;
         at += span_of<U::TOK>(a.span, __ldg(a.c.lens + b)).n * per_seq;
       }
-      if (threadIdx.x == 32 * kWarps - 1) a.prefix[n] = before + sum;
+      if (threadIdx.x == kThreads - 1) a.prefix[n] = before + sum;
     }
     __syncthreads();
-    const Deal d(pre[256], gridDim.x);
+    const Deal d(pre[kThreads], gridDim.x * kWarps);
     wid = warp * gridDim.x + blockIdx.x;  // a short list is spread over the SMs first
     if (wid >= d.warps) return;
     r0 = d.begin(wid);
@@ -262,7 +287,7 @@ __global__ void __launch_bounds__(32 * kWarps, MINB) cache_attn_kernel(const Dec
       x.begin = 0;
       x.s = span_of<U::TOK>(a.span, x.len);
     } else {
-      int lo = 0, hi = 255;  // the last run of sequences that begins at or before u
+      int lo = 0, hi = kThreads - 1;  // the last run of sequences that begins at or before u
       while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
         if (pre[mid] <= u)
@@ -289,7 +314,8 @@ __global__ void __launch_bounds__(32 * kWarps, MINB) cache_attn_kernel(const Dec
   auto first_token = [&](const Item& x, int k) { return (k < x.s.sinks ? k : x.s.lo + k - x.s.sinks) * U::TOK; };
 
   bool dead = false;
-  int issued = 0, used = 0;  // units copied and consumed by this warp (ring stages)
+  int st_in = 0, st_out = 0;  // ring stages of the next copy and of the next unit
+  uint32_t ph_out = 0;
   unsigned bad = 0;          // bit per stage: no such page, the unit's keys are masked
   const int items = n * per_seq;
   for (int at = WHOLE ? static_cast<int>(blockIdx.x) : r0; at < (WHOLE ? items : r1);) {
@@ -301,14 +327,16 @@ __global__ void __launch_bounds__(32 * kWarps, MINB) cache_attn_kernel(const Dec
     const int count = max(0, (k1 - k0 + step - 1) / step);
     if (WHOLE && x.head == 0 && x.tile == 0 && threadIdx.x == 0 && a.c.err && x.len > a.span.cap)
       atomicOr(a.c.err, kErrPage);
+    const unsigned char* const head_base = a.c.pages + static_cast<size_t>(x.head) * cache4::Layout<DH>::BLOCK;
+    const int* const table = a.c.table + static_cast<size_t>(x.b) * a.c.max_pages;
+    const unsigned page_bytes = static_cast<unsigned>(a.c.Hkv) * cache4::Layout<DH>::BLOCK;
     int pages = 0;  // of units 32 j .. 32 j + 31, one per lane
     auto copy = [&](int i) {
       if ((i & 31) == 0 && i + lane < count)
-        pages = __ldg(a.c.table + static_cast<size_t>(x.b) * a.c.max_pages +
-                      first_token(x, k0 + (i + lane) * step) / kPage);
+        pages = __ldg(table + first_token(x, k0 + (i + lane) * step) / kPage);
       int page = __shfl_sync(0xffffffffu, pages, i & 31);
-      const int st = issued % kStages;
-      ++issued;
+      const int st = st_in;
+      st_in = st_in + 1 == kStages ? 0 : st_in + 1;
       bad &= ~(1u << st);
       if (page < 0 || page >= a.c.n_pages) {
         if (lane == 0 && a.c.err) atomicOr(a.c.err, kErrPage);
@@ -316,7 +344,7 @@ __global__ void __launch_bounds__(32 * kWarps, MINB) cache_attn_kernel(const Dec
         page = 0;
       }
       if (lane == 0) {
-        const unsigned char* src = a.c.pages + cache4::block_offset<DH>(a.c, page, x.head);
+        const unsigned char* src = head_base + static_cast<unsigned long long>(page) * page_bytes;
         const uint32_t dst = ring_s + st * U::BYTES, bar = bars + 8 * st;
         sm100::mbar_arrive_expect_tx(bar, U::BYTES);
         if constexpr (U::TOK == kPage) {
@@ -394,21 +422,25 @@ __global__ void __launch_bounds__(32 * kWarps, MINB) cache_attn_kernel(const Dec
       }
     }
 
-    float o[NT][MU][4], m[NT][2], l[NT][2];
+    // reference and sum per row; what a score becomes a weight with (s - less) * rs + off
+    float o[NT][MU][4], m[NT][2], mx[NT][2], l[NT][4], less[NT][2], off[NT][2];
+    bool far = false;
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
       m[j][0] = m[j][1] = -INFINITY;
-      l[j][0] = l[j][1] = 0.f;
+      less[j][0] = less[j][1] = 0.f;
+      off[j][0] = off[j][1] = 7.f;
+      l[j][0] = l[j][1] = l[j][2] = l[j][3] = 0.f;
 #pragma unroll
       for (int i = 0; i < MU; ++i) o[j][i][0] = o[j][i][1] = o[j][i][2] = o[j][i][3] = 0.f;
     }
 
     for (int i = 0; i < count; ++i) {
-      const int st = used % kStages;
+      const int st = st_out;
       const int key0 = first_token(x, k0 + i * step);
       const bool gone = (bad >> st) & 1u;
       const unsigned char* const kc = ring + st * U::BYTES;
-      if (!sm100::mbar_wait(bars + 8 * st, (used / kStages) & 1, abort_flag)) dead = true;
+      if (!sm100::mbar_wait(bars + 8 * st, ph_out, abort_flag)) dead = true;
       // S^T: keys g and g + 8 of each tile sit at rows (g >> 1) + 4 (g & 1) and 8 further
       const int rk = (g >> 1) + 4 * (g & 1);
       float s[MT][NT][4];
@@ -435,7 +467,7 @@ __global__ void __launch_bounds__(32 * kWarps, MINB) cache_attn_kernel(const Dec
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               const uint32_t b = DH == 128 ? (i == 0 ? sb[h] & 255u : sb[h] >> 8) : sb[h];
-              sc[h] = scale_pair(b * 0x10001u);
+              sc[h] = scale_pair(b * 0x800080u);
             }
           }
           uint32_t v0[4], v1[4];
@@ -465,48 +497,74 @@ __global__ void __launch_bounds__(32 * kWarps, MINB) cache_attn_kernel(const Dec
               if (gone || key > p || (p - key >= a.span.window && key >= a.span.sinks)) s[mt][j][i] = -INFINITY;
             }
       }
-      uint32_t pb[MT][NT][TERMS][2];
+      // The rows' references are raised only when some score passes one by more than 2^8: most units
+      // need no exchange between lanes and leave O as it is. Weights are 2^7 .. 2^15 at most.
+      bool above = false;
 #pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        float ref[2], corr[2];
+      for (int j = 0; j < NT; ++j)
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          float mx = fmaxf(s[0][j][c], s[0][j][c + 2]);
+          mx[j][c] = fmaxf(s[0][j][c], s[0][j][c + 2]);
 #pragma unroll
-          for (int mt = 1; mt < MT; ++mt) mx = fmaxf(mx, fmaxf(s[mt][j][c], s[mt][j][c + 2]));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-          const float mn = fmaxf(m[j][c], mx);
-          ref[c] = mn == -INFINITY ? 0.f : mn;  // nothing seen yet: weights 2^-inf = 0
-          corr[c] = ex2((m[j][c] - ref[c]) * rs[j][c]);
-          m[j][c] = mn;
-          l[j][c] *= corr[c];
+          for (int mt = 1; mt < MT; ++mt) mx[j][c] = max3(mx[j][c], s[mt][j][c], s[mt][j][c + 2]);
+          above |= (mx[j][c] - m[j][c]) * rs[j][c] > 8.f;  // -inf less -inf: no
         }
-        if (__any_sync(0xffffffffu, corr[0] != 1.f || corr[1] != 1.f)) {
+      if (__any_sync(0xffffffffu, above)) {
+        far = false;
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          float corr[2];
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            float top = mx[j][c];
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+            top = fmaxf(top, m[j][c]);
+            const float ref = top == -INFINITY ? 0.f : top;  // nothing seen yet: weights 2^-inf = 0
+            corr[c] = ex2((m[j][c] - ref) * rs[j][c]);
+            m[j][c] = top;
+            // s * rs - ref * rs in one rounding is off by 2^-24 of ref * rs: where that is large the
+            // difference is taken first
+            const bool big = fabsf(ref * rs[j][c]) > 1048576.f;
+            far |= big;
+            less[j][c] = big ? ref : 0.f;
+            off[j][c] = big ? 7.f : 7.f - ref * rs[j][c];
+          }
 #pragma unroll
           for (int i = 0; i < MU; ++i) {
             o[j][i][0] *= corr[0], o[j][i][1] *= corr[1];
             o[j][i][2] *= corr[0], o[j][i][3] *= corr[1];
           }
+          l[j][0] *= corr[0], l[j][1] *= corr[1];
         }
+        far = __any_sync(0xffffffffu, far);
+      }
+      if (far) {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s[mt][j][i] -= less[j][i & 1];
+      }
+      uint32_t pb[MT][NT][TERMS][2];
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
-          float p[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            // the difference first: exact for the largest, however large the scores are
-            p[i] = ex2(fmaf(s[mt][j][i] - ref[i & 1], rs[j][i & 1], 15.f));
-            l[j][i & 1] += p[i];
-          }
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            pb[mt][j][0][h] = transpose8(pack2<__half>(p[2 * h], p[2 * h + 1]));
-            if constexpr (SPLIT)
-              pb[mt][j][1][h] = transpose8(pack2<__half>(lo_term<__half>(p[2 * h]), lo_term<__half>(p[2 * h + 1])));
+            fma_pair(s[mt][j][2 * h], s[mt][j][2 * h + 1], rs[j][0], rs[j][1], off[j][0], off[j][1]);
+            const float p0 = ex2(s[mt][j][2 * h]), p1 = ex2(s[mt][j][2 * h + 1]);
+            pb[mt][j][0][h] = transpose8(pack2<__half>(p0, p1));
+            if constexpr (SPLIT) pb[mt][j][1][h] = transpose8(pack2<__half>(lo_term<__half>(p0), lo_term<__half>(p1)));
           }
+          // the rows' sums, of the weights as O takes them: a product with ones
+#pragma unroll
+          for (int e = 0; e < TERMS; ++e)
+            mma(l[j], 0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u, pb[mt][j][e][0], pb[mt][j][e][1]);
         }
-      }
       // O^T += V^T P^T: keys 2t, 2t + 1, 2t + 8, 2t + 9 of a tile sit at rows t, t + 4, t + 8, t + 12
       const unsigned char* const vc = kc + U::V_OFF;
 #pragma unroll
@@ -523,7 +581,8 @@ __global__ void __launch_bounds__(32 * kWarps, MINB) cache_attn_kernel(const Dec
           sb[k] = vc[U::CODES + r * (DH / 16) + (DH == 128 ? g : DH == 64 ? g >> 1 : g >> 2)];
           if (edge && (gone || r >= behind)) sb[k] = 0;  // no token there: bytes of any kind
         }
-        const Scale sa = scale_pair(sb[0] + sb[1] * 0x10000u), sz = scale_pair(sb[2] + sb[3] * 0x10000u);
+        const Scale sa = scale_pair((sb[0] + sb[1] * 0x10000u) * 128u),
+                    sz = scale_pair((sb[2] + sb[3] * 0x10000u) * 128u);
 #pragma unroll
         for (int i = 0; i < WV; ++i)
 #pragma unroll
@@ -543,18 +602,16 @@ __global__ void __launch_bounds__(32 * kWarps, MINB) cache_attn_kernel(const Dec
           }
       }
       __syncwarp();  // every lane has read the stage
-      ++used;
+      if (++st_out == kStages) {
+        st_out = 0;
+        ph_out ^= 1u;
+      }
       if (i + kStages < count) copy(i + kStages);
     }
 #pragma unroll
     for (int j = 0; j < NT; ++j)
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        l[j][c] += __shfl_xor_sync(0xffffffffu, l[j][c], 4);
-        l[j][c] += __shfl_xor_sync(0xffffffffu, l[j][c], 8);
-        l[j][c] += __shfl_xor_sync(0xffffffffu, l[j][c], 16);
-        m[j][c] *= rs[j][c];  // in powers of 2
-      }
+      for (int c = 0; c < 2; ++c) m[j][c] *= rs[j][c];  // in powers of 2
     auto out_row = [&](int rr) {
       const int tok = rr / a.group, hd = rr - tok * a.group;
       return static_cast<T*>(a.out) + ((static_cast<size_t>(x.b) * a.n_q + tok) * a.H + x.head * a.group + hd) * DH;
@@ -586,7 +643,7 @@ __global__ void __launch_bounds__(32 * kWarps, MINB) cache_attn_kernel(const Dec
                 make_float2(o[j][i][c] * by, o[j][i][c + 2] * by);
         }
         __syncthreads();
-        for (int e = threadIdx.x; e < 8 * DH / 4; e += 32 * kWarps) {
+        for (int e = threadIdx.x; e < 8 * DH / 4; e += kThreads) {
           const int row = e / (DH / 4), ch = (e - row * (DH / 4)) * 4;
           const int rr = (x.tile * NT + j) * 8 + row;
           if (rr >= a.rows) continue;
@@ -620,27 +677,24 @@ __global__ void __launch_bounds__(32 * kWarps, MINB) cache_attn_kernel(const Dec
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           const int row = 8 * j + 2 * t + c, rr = x.tile * NT * 8 + row;
+          if (!all && g == 0) {  // all rows: half a sector would have to be filled from memory when read
+            part[8 * NT * DH + row] = m[j][c];
+            part[8 * NT * (DH + 1) + row] = l[j][c];
+          }
           if (rr >= a.rows) continue;
-          if (all) {
-            T* dst = out_row(rr) + g * (DH / 8);
-            const float inv = l[j][c] == 0.f ? 0.f : kCodeScale / l[j][c];
+          const float by = !all ? 1.f : l[j][c] == 0.f ? 0.f : kCodeScale / l[j][c];
+          float* const pd = part + row * DH + g * (DH / 8);
+          T* const dst = out_row(rr) + g * (DH / 8);
 #pragma unroll
-            for (int i = 0; i < MU; ++i) {
-              const float v0 = o[j][i][c] * inv, v1 = o[j][i][c + 2] * inv;
-              if constexpr (SPLIT)
-                *reinterpret_cast<float2*>(dst + 2 * i) = make_float2(v0, v1);
-              else
-                *reinterpret_cast<uint32_t*>(dst + 2 * i) = pack2<T>(v0, v1);
-            }
-          } else {
-#pragma unroll
-            for (int i = 0; i < MU; ++i)
-              *reinterpret_cast<float2*>(part + row * DH + g * (DH / 8) + 2 * i) =
-                  make_float2(o[j][i][c], o[j][i][c + 2]);
-            if (g == 0) {
-              part[8 * NT * DH + row] = m[j][c];
-              part[8 * NT * (DH + 1) + row] = l[j][c];
-            }
+          for (int i = 0; i < MU; i += 2) {
+            const float v0 = o[j][i][c] * by, v1 = o[j][i][c + 2] * by;
+            const float v2 = o[j][i + 1][c] * by, v3 = o[j][i + 1][c + 2] * by;
+            if (!all)
+              *reinterpret_cast<float4*>(pd + 2 * i) = make_float4(v0, v1, v2, v3);
+            else if constexpr (SPLIT)
+              *reinterpret_cast<float4*>(dst + 2 * i) = make_float4(v0, v1, v2, v3);
+            else
+              *reinterpret_cast<uint2*>(dst + 2 * i) = make_uint2(pack2<T>(v0, v1), pack2<T>(v2, v3));
           }
         }
       at = x.begin + k1;
@@ -648,27 +702,27 @@ __global__ void __launch_bounds__(32 * kWarps, MINB) cache_attn_kernel(const Dec
   }
   if (dead) {
     if (lane == 0 && a.c.err) atomicOr(a.c.err, kErrTimeoutEpilogue);
-    for (int k = max(used - kStages, 0); k < issued; ++k)
-      sm100::mbar_wait_drain(bars + 8 * (k % kStages), (k / kStages) & 1);
+    // let the copies in flight land before the CTA's shared memory goes away: stages from st_out on
+    // are in phase ph_out, those before it in the next; waiting for both parities covers either
+    for (int k = 0; k < 2 * kStages; ++k) sm100::mbar_wait_drain(bars + 8 * (k >> 1), k & 1);
   }
 }
 
 // Rows of items that several warps shared: their parts added in the order of the keys. Rows that
-// see nothing: zeros. One CTA per row; its eight warps take a range of the parts each.
+// see nothing: zeros. A CTA takes `per` rows of an item (gridDim.y slices): one thread per four
+// channels of a row and per group of consecutive parts, so that the loads of many parts are in
+// flight at once; then neighbouring groups are added, in a fixed tree.
 template <int DH, typename T, int NT>
-__global__ void __launch_bounds__(256) cache_attn_join_kernel(const DecodeArgs a, int ctas) {
+__global__ void __launch_bounds__(1024) cache_attn_join_kernel(const DecodeArgs a, int grid_warps, int per) {
   pdl_trigger();
   pdl_wait();
-  constexpr int C = DH / 32, JW = 8;
-  __shared__ float sums[JW], sacc[JW][DH], stop[JW];
-  const int rows = a.rows, per_seq = a.c.Hkv * rows;
-  const int b = blockIdx.x / per_seq, hr = blockIdx.x - b * per_seq;
-  const int head = hr / rows, rr = hr - head * rows;
-  const int tile = rr / (8 * NT), row = rr - tile * 8 * NT;
-  const int at = a.prefix[b], units = a.prefix[a.c.n_seqs];
-  const int n = (a.prefix[b + 1] - at) / (a.c.Hkv * a.tiles);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const Deal d(units, ctas);
+  __shared__ float top_s[1024], sum_s[1024];
+  __shared__ float4 acc_s[1024];
+  const int tile = blockIdx.x % a.tiles, bh = blockIdx.x / a.tiles;
+  const int b = bh / a.c.Hkv, head = bh - b * a.c.Hkv;
+  const int at = a.prefix[b], after = a.prefix[b + 1], units = a.prefix[a.c.n_seqs];
+  const int n = (after - at) / (a.c.Hkv * a.tiles);
+  const Deal d(units, grid_warps);
   const int begin = at + (head * a.tiles + tile) * n;
   int w0 = 0, w1 = -1;
   if (n > 0) {
@@ -676,59 +730,65 @@ __global__ void __launch_bounds__(256) cache_attn_join_kernel(const DecodeArgs a
     w1 = d.warp_of(begin + n - 1);
     if (w0 == w1) return;  // that warp wrote the result
   }
-  auto part_of = [&](int w) {
-    const int first = d.begin(w);
-    return a.parts + static_cast<size_t>(2 * w + (begin <= first ? 0 : 1)) * (DH + 2) * 8 * NT;
-  };
-  const int each = (w1 - w0 + JW) / JW, from = w0 + warp * each, to = min(from + each, w1 + 1);
-  float acc[C], sum = 0.f, top = -INFINITY;
+  constexpr int PART = (DH + 2) * 8 * NT, QUADS = DH / 4;
+  const int lanes = per * QUADS, groups = blockDim.x / lanes;  // threads of a group of parts
+  const int t = threadIdx.x, group = t / lanes, e = t - group * lanes;
+  const int row = blockIdx.y * per + e / QUADS, ch = (e % QUADS) * 4;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  float sum = 0.f, top = -INFINITY;
+  if (group < groups) {
+    const int each = (w1 - w0 + groups) / groups, from = w0 + group * each, to = min(from + each, w1 + 1);
+    const bool second = begin > d.begin(w0);  // the first part is its warp's second stretch
+    for (int w = from; w < to; w += 4) {
+      float mw[4], lw[4];
+      float4 v[4];
 #pragma unroll
-  for (int i = 0; i < C; ++i) acc[i] = 0.f;
-  for (int w = from; w < to; w += 32) {
-    // 32 parts at a time: a lane's own maximum and sum, then every part's output
-    const bool on = w + lane < to;
-    const float* p = part_of(on ? w + lane : w);
-    const float mw = on ? p[8 * NT * DH + row] : -INFINITY, lw = on ? p[8 * NT * (DH + 1) + row] : 0.f;
-    float mx = mw;
+      for (int k = 0; k < 4; ++k) {
+        const int x = min(w + k, to - 1);
+        const float* p = a.parts + static_cast<size_t>(2 * x + (x == w0 && second ? 1 : 0)) * PART;
+        mw[k] = p[8 * NT * DH + row];
+        lw[k] = p[8 * NT * (DH + 1) + row];
+        v[k] = *reinterpret_cast<const float4*>(p + row * DH + ch);
+      }
 #pragma unroll
-    for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    const float up = fmaxf(top, mx);
-    const float keep = top == -INFINITY ? 0.f : ex2(top - up), by = mw == -INFINITY ? 0.f : ex2(mw - up);
-    top = up;
-    sum *= keep;
-#pragma unroll
-    for (int i = 0; i < C; ++i) acc[i] *= keep;
-    const int many = min(32, to - w);
-#pragma unroll 4
-    for (int k = 0; k < many; ++k) {
-      const float f = __shfl_sync(0xffffffffu, by, k);
-      sum = fmaf(__shfl_sync(0xffffffffu, lw, k), f, sum);
-      const float* q = part_of(w + k) + row * DH + lane;
-#pragma unroll
-      for (int i = 0; i < C; ++i) acc[i] = fmaf(q[32 * i], f, acc[i]);
+      for (int k = 0; k < 4; ++k) {
+        if (w + k >= to) break;
+        const float up = fmaxf(top, mw[k]);
+        const float keep = top == -INFINITY ? 0.f : ex2(top - up), by = mw[k] == -INFINITY ? 0.f : ex2(mw[k] - up);
+        top = up;
+        sum = fmaf(lw[k], by, sum * keep);
+        acc.x = fmaf(v[k].x, by, acc.x * keep), acc.y = fmaf(v[k].y, by, acc.y * keep);
+        acc.z = fmaf(v[k].z, by, acc.z * keep), acc.w = fmaf(v[k].w, by, acc.w * keep);
+      }
     }
   }
-  if (lane == 0) {
-    sums[warp] = sum;
-    stop[warp] = top;
-  }
-#pragma unroll
-  for (int i = 0; i < C; ++i) sacc[warp][32 * i + lane] = acc[i];
-  __syncthreads();
-  if (threadIdx.x < DH) {
-    float tt = -INFINITY, ss = 0.f, v = 0.f;
-#pragma unroll
-    for (int w = 0; w < JW; ++w) tt = fmaxf(tt, stop[w]);
-#pragma unroll
-    for (int w = 0; w < JW; ++w) {
-      const float f = stop[w] == -INFINITY ? 0.f : ex2(stop[w] - tt);
-      ss = fmaf(sums[w], f, ss);
-      v = fmaf(sacc[w][threadIdx.x], f, v);
+  top_s[t] = top;
+  sum_s[t] = sum;
+  acc_s[t] = acc;
+  for (int s = 1; s < groups; s *= 2) {
+    __syncthreads();
+    const int o = t + s * lanes;
+    if (group % (2 * s) == 0 && group + s < groups) {
+      const float mo = top_s[o], up = fmaxf(top, mo);
+      const float keep = top == -INFINITY ? 0.f : ex2(top - up), by = mo == -INFINITY ? 0.f : ex2(mo - up);
+      const float4 v = acc_s[o];
+      sum = fmaf(sum_s[o], by, sum * keep);
+      acc.x = fmaf(v.x, by, acc.x * keep), acc.y = fmaf(v.y, by, acc.y * keep);
+      acc.z = fmaf(v.z, by, acc.z * keep), acc.w = fmaf(v.w, by, acc.w * keep);
+      top_s[t] = top = up;
+      sum_s[t] = sum;
+      acc_s[t] = acc;
     }
-    const int tok = rr / a.group, hd = rr - tok * a.group;
-    static_cast<T*>(a.out)[((static_cast<size_t>(b) * a.n_q + tok) * a.H + head * a.group + hd) * DH + threadIdx.x] =
-        from_f32<T>(ss == 0.f ? 0.f : v * (kCodeScale / ss));
   }
+  const int rr = tile * 8 * NT + row;
+  if (group != 0 || row >= 8 * NT || rr >= a.rows) return;
+  const int tok = rr / a.group, hd = rr - tok * a.group;
+  T* dst = static_cast<T*>(a.out) + ((static_cast<size_t>(b) * a.n_q + tok) * a.H + head * a.group + hd) * DH + ch;
+  const float inv = sum == 0.f ? 0.f : kCodeScale / sum;
+  if constexpr (std::is_same_v<T, float>)
+    *reinterpret_cast<float4*>(dst) = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+  else
+    *reinterpret_cast<uint2*>(dst) = make_uint2(pack2<T>(acc.x * inv, acc.y * inv), pack2<T>(acc.z * inv, acc.w * inv));
 }
 
 int tile_rows(int rows, bool bf16) { return bf16 && rows > 8 ? 16 : 8; }
@@ -744,22 +804,26 @@ long long most_units(int max_pages, int n_q, int dh, int window, int sinks) {
 struct Plan {
   bool whole;
   long long items, units;
-  int ctas;
+  int ctas, warps;  // warps: of the grid, when they share a list of units
 };
-Plan plan_of(int n_seqs, int max_pages, int n_q, int tiles, int Hkv, int dh, int window, int sinks) {
+Plan plan_of(int n_seqs, int max_pages, int n_q, int tiles, int Hkv, int dh, int window, int sinks,
+             int cta_warps) {
   Plan p;
   const long long most = most_units(max_pages, n_q, dh, window, sinks);
   p.items = static_cast<long long>(n_seqs) * Hkv * tiles;
   p.units = p.items * most;
   p.whole = most <= kWholeUnits;
-  const long long want = p.whole ? p.items : (p.units + kWarps * kLeastUnits - 1) / (kWarps * kLeastUnits);
-  p.ctas = static_cast<int>(want < kMaxCtas ? want : kMaxCtas);
+  const long long cap = 148;  // one per SM
+  const long long want =
+      p.whole ? p.items : (p.units + static_cast<long long>(cta_warps) * kLeastUnits - 1) / (cta_warps * kLeastUnits);
+  p.ctas = static_cast<int>(want < cap ? want : cap);
+  p.warps = p.ctas * cta_warps;
   return p;
 }
 
 template <int DH, typename T, int NT>
 cudaError_t launch_decode(const CacheAttnArgs& c, cudaStream_t st) {
-  constexpr int MINB = DH == 128 && NT == 2 ? 1 : 2;
+  constexpr int kWarps = Shape<DH, NT>::WARPS;
   DecodeArgs a{};
   a.c = c.c;
   a.span = {c.c.max_pages * kPage, c.n_q, c.window, c.sinks};
@@ -767,18 +831,30 @@ cudaError_t launch_decode(const CacheAttnArgs& c, cudaStream_t st) {
   a.n_q = c.n_q, a.H = c.H, a.group = c.H / c.c.Hkv;
   a.rows = c.n_q * a.group;
   a.tiles = (a.rows + 8 * NT - 1) / (8 * NT);
-  const Plan p = plan_of(c.c.n_seqs, c.c.max_pages, c.n_q, a.tiles, c.c.Hkv, DH, c.window, c.sinks);
-  auto kernel = p.whole ? cache_attn_kernel<DH, T, NT, true, MINB> : cache_attn_kernel<DH, T, NT, false, MINB>;
+  const Plan p = plan_of(c.c.n_seqs, c.c.max_pages, c.n_q, a.tiles, c.c.Hkv, DH, c.window, c.sinks, kWarps);
+  auto kernel = p.whole ? cache_attn_kernel<DH, T, NT, true> : cache_attn_kernel<DH, T, NT, false>;
   const int smem = p.whole ? DecodeSmem<DH, NT, true>::BYTES : DecodeSmem<DH, NT, false>::BYTES;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   if (!p.whole) {
     a.parts = static_cast<float*>(c.ws);
-    a.prefix = reinterpret_cast<int*>(a.parts + static_cast<size_t>(2 * kWarps) * p.ctas * (DH + 2) * 8 * NT);
+    a.prefix = reinterpret_cast<int*>(a.parts + static_cast<size_t>(2) * p.warps * (DH + 2) * 8 * NT);
   }
   e = launch_pdl(kernel, dim3(p.ctas), dim3(32 * kWarps), smem, st, a);
-  if (e == cudaSuccess && !p.whole)
-    e = launch_pdl(cache_attn_join_kernel<DH, T, NT>, dim3(c.c.n_seqs * c.c.Hkv * a.rows), dim3(256), 0, st, a, p.ctas);
+  if (e == cudaSuccess && !p.whole) {
+    // many items: their rows together in 256 threads, one to four parts at a time; few: a row per
+    // CTA, with as many threads as it may have
+    const bool many = p.items >= 64;
+    int per = 8 * NT < a.rows ? 8 * NT : a.rows;
+    if (!many)
+      per = 1;
+    else if (per * (DH / 4) > 256)
+      per = 256 / (DH / 4);
+    const int most_rows = 8 * NT < a.rows ? 8 * NT : a.rows;
+    e = launch_pdl(cache_attn_join_kernel<DH, T, NT>,
+                   dim3(static_cast<unsigned>(p.items), (most_rows + per - 1) / per), dim3(many ? 256 : 1024), 0, st, a,
+                   p.warps, per);
+  }
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
@@ -797,9 +873,9 @@ size_t cache_attention_workspace(int n_seqs, int max_pages, int n_q, int H, int 
   const int rows = n_q * (H / Hkv);
   for (int bf16 = 0; bf16 < 2; ++bf16) {
     const int tr = tile_rows(rows, bf16), tiles = (rows + tr - 1) / tr;
-    const Plan p = plan_of(n_seqs, max_pages, n_q, tiles, Hkv, dh, window, sinks);
+    const Plan p = plan_of(n_seqs, max_pages, n_q, tiles, Hkv, dh, window, sinks, 16);
     if (p.units > 0x7fffffffLL) return 0;
-    const size_t bytes = p.whole ? 0 : static_cast<size_t>(2 * kWarps) * p.ctas * (dh + 2) * tr * 4;
+    const size_t bytes = p.whole ? 0 : static_cast<size_t>(2) * kMaxWarps * (dh + 2) * tr * 4;
     most = bytes > most ? bytes : most;
   }
   return most + (static_cast<size_t>(n_seqs) + 1) * 4;
