@@ -18,8 +18,8 @@
 // (mma.sync m16n8k16, f16 operands, fp32 sums: the codes turn into operands in registers, and tcgen05
 // would have them pass through shared memory again, four times their bytes). A code's nibble
 // or-ed into the f16 pattern of 64 is 64 + (q + 8); times the scale minus 72 scales is q * scale,
-// exact, in one fused operation for two codes (dequant). Scales are taken at 2^-4 of their value so that 72 of
-// them stay in f16's range; the factor comes back with the row's scale and at the end. A lane takes 16
+// exact, in one fused operation for two codes (dequant). Scales are taken at 2^-7 of their value; the
+// factor comes back with the row's scale and at the end. A lane takes 16
 // (or 8, or 32) consecutive channels of a key, since the order of a dot product's terms is free as long as
 // Q has the same one, and for V eight neighbouring lanes' keys are chosen so that the reads of a warp are
 // whole lines of shared memory. P^T turns from accumulator to operand layout by
@@ -39,7 +39,8 @@ using cache4::kPage;
 constexpr int kMaxWarps = 148 * 16;  // that share a list of units: 16 per SM
 constexpr int kLeastUnits = 4;   // of a warp's stretch
 constexpr int kWholeUnits = 32;  // items up to this many units are not split
-constexpr float kCodeScale = 16.f;  // operands hold 2^-4 of a value
+constexpr float kCodeScale = 128.f;  // operands hold 2^-7 of a value
+constexpr uint32_t kWideScale = 224;  // scale bytes from here on take the exact way (dequant)
 
 template <int DH>
 struct Unit {
@@ -129,17 +130,18 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
   return r;
 }
 
-// Two scales (f16 bits in the low and high half of b) as pairs: 2^-4 of the scales (x), -72 (y) and -8
-// (z) times that.
+// Two scales (f16 bits in the low and high half of b) as pairs: 2^-7 of the scales (x), and what
+// takes the offset of a high nibble (y) and of a low one (z) away again.
 struct Scale {
   __half2 x, y, z;
 };
+template <bool WIDE>
 __device__ __forceinline__ Scale scale_pair(uint32_t b) {
   Scale s;
   const __half2 f = as_h2(b);
   s.x = __hmul2(f, __float2half2_rn(1.f / kCodeScale));
   s.y = __hmul2(f, __float2half2_rn(-72.f / kCodeScale));
-  s.z = __hmul2(f, __float2half2_rn(-8.f / kCodeScale));
+  s.z = __hmul2(f, __float2half2_rn((WIDE ? -8.f : -1032.f) / kCodeScale));
   return s;
 }
 __device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t b, uint32_t c) {
@@ -148,15 +150,21 @@ __device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t b, uint32_t c) {
   return r;
 }
 // The codes j of the low and of the high half of w, j = 0..3, times their scales. A byte's high
-// nibble h sits where it counts units of 64's f16 pattern: 64 + h; the byte in 1024's: 1024 + l + 16 h,
-// less 16 (64 + h) is its low nibble. That takes one shift per word instead of three (shifts and
-// logic run at half the rate of the fused multiply-adds, and are what bounds the kernel).
+// nibble h sits where it counts units of 64's f16 pattern: 64 + h, and its low one l where it
+// counts those of 1024: 1024 + l. (64 + h) s - 72 s and (1024 + l) s - 1032 s are exact in one fused
+// operation, since 72 and 1032 times a scale have at most 11 significant bits (1032 = 8 * 129, 129 * 15 <
+// 2048) and at 2^-7 of the scale neither end of the format leaves f16's range -- but for the two
+// largest scales, 8192 and 9216, whose 1032nd overflows. WIDE takes the low nibble as
+// (1024 + l + 16 h) - 16 (64 + h) first, one operation more, for those.
+// One shift per word: shifts and logic (the ALU pipe) and half2 operations (the heavy half of
+// the FMA pipe) both issue every other cycle, and are what bounds the kernel.
+template <bool WIDE>
 __device__ __forceinline__ void dequant(uint32_t w, const Scale& s, uint32_t (&v)[4]) {
-  const __half2 less = __float2half2_rn(-16.f);
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const __half2 h = as_h2(and_or(w, 0x00F000F0u, 0x54005400u));
-    const __half2 l = __hfma2(h, less, as_h2(and_or(w, 0x00FF00FFu, 0x64006400u)));
+    __half2 l = as_h2(and_or(w, WIDE ? 0x00FF00FFu : 0x000F000Fu, 0x64006400u));
+    if (WIDE) l = __hfma2(h, __float2half2_rn(-16.f), l);
     v[2 * i] = h2(__hfma2(l, s.x, s.z));
     v[2 * i + 1] = h2(__hfma2(h, s.x, s.y));
     w >>= 8;
@@ -425,188 +433,213 @@ __global__ void __launch_bounds__(32 * Shape<DH, NT>::WARPS, 1) cache_attn_kerne
     // reference and sum per row; what a score becomes a weight with (s - less) * rs + off
     float o[NT][MU][4], m[NT][2], mx[NT][2], l[NT][4], less[NT][2], off[NT][2];
     bool far = false;
+    uint32_t top_scale = 0;  // the largest of the keys' scale bytes
+    auto clear = [&]() {
+      far = false;
 #pragma unroll
-    for (int j = 0; j < NT; ++j) {
-      m[j][0] = m[j][1] = -INFINITY;
-      less[j][0] = less[j][1] = 0.f;
-      off[j][0] = off[j][1] = 7.f;
-      l[j][0] = l[j][1] = l[j][2] = l[j][3] = 0.f;
+      for (int j = 0; j < NT; ++j) {
+        m[j][0] = m[j][1] = -INFINITY;
+        less[j][0] = less[j][1] = 0.f;
+        off[j][0] = off[j][1] = 7.f;
+        l[j][0] = l[j][1] = l[j][2] = l[j][3] = 0.f;
 #pragma unroll
-      for (int i = 0; i < MU; ++i) o[j][i][0] = o[j][i][1] = o[j][i][2] = o[j][i][3] = 0.f;
-    }
-
-    for (int i = 0; i < count; ++i) {
-      const int st = st_out;
-      const int key0 = first_token(x, k0 + i * step);
-      const bool gone = (bad >> st) & 1u;
-      const unsigned char* const kc = ring + st * U::BYTES;
-      if (!sm100::mbar_wait(bars + 8 * st, ph_out, abort_flag)) dead = true;
-      // S^T: keys g and g + 8 of each tile sit at rows (g >> 1) + 4 (g & 1) and 8 further
-      const int rk = (g >> 1) + 4 * (g & 1);
-      float s[MT][NT][4];
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-#pragma unroll
-        for (int j = 0; j < NT; ++j) s[mt][j][0] = s[mt][j][1] = s[mt][j][2] = s[mt][j][3] = 0.f;
-        uint32_t w[2][WK];
-        uint32_t sb[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int r = 16 * mt + rk + 8 * h;
-          lds_words<WK>(kc + r * (DH / 2) + t * (DH / 8), w[h]);
-          const unsigned char* sp = kc + U::CODES + r * (DH / 16);
-          if constexpr (DH == 128)
-            sb[h] = *reinterpret_cast<const unsigned short*>(sp + 2 * t);
-          else
-            sb[h] = sp[DH == 64 ? t : t >> 1];
-        }
-        Scale sc[2];
-#pragma unroll
-        for (int i = 0; i < WK; ++i) {
-          if (i == 0 || (DH == 128 && i == 2)) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const uint32_t b = DH == 128 ? (i == 0 ? sb[h] & 255u : sb[h] >> 8) : sb[h];
-              sc[h] = scale_pair(b * 0x800080u);
-            }
-          }
-          uint32_t v0[4], v1[4];
-          dequant(w[0][i], sc[0], v0);
-          dequant(w[1][i], sc[1], v1);
-#pragma unroll
-          for (int j = 0; j < NT; ++j)
-#pragma unroll
-            for (int e = 0; e < TERMS; ++e) {
-              mma(s[mt][j], v0[0], v1[0], v0[1], v1[1], q[j][e][2 * i][0], q[j][e][2 * i][1]);
-              mma(s[mt][j], v0[2], v1[2], v0[3], v1[3], q[j][e][2 * i + 1][0], q[j][e][2 * i + 1][1]);
-            }
-        }
+        for (int i = 0; i < MU; ++i) o[j][i][0] = o[j][i][1] = o[j][i][2] = o[j][i][3] = 0.f;
       }
-      // mask: units that hold keys after some row's position, or before some row's window
-      const int behind = len - key0;  // rows of the unit that hold tokens
-      const bool edge = gone || key0 + U::TOK - 1 > first_pos ||
-                        (len - 1 - key0 >= a.span.window && key0 + U::TOK > a.span.sinks);
-      if (edge) {
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-          for (int j = 0; j < NT; ++j)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int key = key0 + 16 * mt + rk + 8 * (i >> 1), p = pos[j][i & 1];
-              if (gone || key > p || (p - key >= a.span.window && key >= a.span.sinks)) s[mt][j][i] = -INFINITY;
-            }
-      }
-      // The rows' references are raised only when some score passes one by more than 2^8: most units
-      // need no exchange between lanes and leave O as it is. Weights are 2^7 .. 2^15 at most.
-      bool above = false;
-#pragma unroll
-      for (int j = 0; j < NT; ++j)
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          mx[j][c] = fmaxf(s[0][j][c], s[0][j][c + 2]);
-#pragma unroll
-          for (int mt = 1; mt < MT; ++mt) mx[j][c] = max3(mx[j][c], s[mt][j][c], s[mt][j][c + 2]);
-          above |= (mx[j][c] - m[j][c]) * rs[j][c] > 8.f;  // -inf less -inf: no
-        }
-      if (__any_sync(0xffffffffu, above)) {
-        far = false;
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          float corr[2];
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            float top = mx[j][c];
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-            top = fmaxf(top, m[j][c]);
-            const float ref = top == -INFINITY ? 0.f : top;  // nothing seen yet: weights 2^-inf = 0
-            corr[c] = ex2((m[j][c] - ref) * rs[j][c]);
-            m[j][c] = top;
-            // s * rs - ref * rs in one rounding is off by 2^-24 of ref * rs: where that is large the
-            // difference is taken first
-            const bool big = fabsf(ref * rs[j][c]) > 1048576.f;
-            far |= big;
-            less[j][c] = big ? ref : 0.f;
-            off[j][c] = big ? 7.f : 7.f - ref * rs[j][c];
-          }
-#pragma unroll
-          for (int i = 0; i < MU; ++i) {
-            o[j][i][0] *= corr[0], o[j][i][1] *= corr[1];
-            o[j][i][2] *= corr[0], o[j][i][3] *= corr[1];
-          }
-          l[j][0] *= corr[0], l[j][1] *= corr[1];
-        }
-        far = __any_sync(0xffffffffu, far);
-      }
-      if (far) {
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-          for (int j = 0; j < NT; ++j)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) s[mt][j][i] -= less[j][i & 1];
-      }
-      uint32_t pb[MT][NT][TERMS][2];
-#pragma unroll
-      for (int j = 0; j < NT; ++j)
+    };
+    auto pass = [&](auto wide) {
+      constexpr bool WIDE = decltype(wide)::value;
+      for (int i = 0; i < count; ++i) {
+        const int st = st_out;
+        const int key0 = first_token(x, k0 + i * step);
+        const bool gone = (bad >> st) & 1u;
+        const unsigned char* const kc = ring + st * U::BYTES;
+        if (!sm100::mbar_wait(bars + 8 * st, ph_out, abort_flag)) dead = true;
+        // mask: units that hold keys after some row's position, or before some row's window
+        const int behind = len - key0;  // rows of the unit that hold tokens
+        const bool edge = gone || key0 + U::TOK - 1 > first_pos ||
+                          (len - 1 - key0 >= a.span.window && key0 + U::TOK > a.span.sinks);
+        // S^T: keys g and g + 8 of each tile sit at rows (g >> 1) + 4 (g & 1) and 8 further
+        const int rk = (g >> 1) + 4 * (g & 1);
+        float s[MT][NT][4];
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
+          for (int j = 0; j < NT; ++j) s[mt][j][0] = s[mt][j][1] = s[mt][j][2] = s[mt][j][3] = 0.f;
+          uint32_t w[2][WK];
+          uint32_t sb[2];
+#pragma unroll
           for (int h = 0; h < 2; ++h) {
-            fma_pair(s[mt][j][2 * h], s[mt][j][2 * h + 1], rs[j][0], rs[j][1], off[j][0], off[j][1]);
-            const float p0 = ex2(s[mt][j][2 * h]), p1 = ex2(s[mt][j][2 * h + 1]);
-            pb[mt][j][0][h] = transpose8(pack2<__half>(p0, p1));
-            if constexpr (SPLIT) pb[mt][j][1][h] = transpose8(pack2<__half>(lo_term<__half>(p0), lo_term<__half>(p1)));
+            const int r = 16 * mt + rk + 8 * h;
+            lds_words<WK>(kc + r * (DH / 2) + t * (DH / 8), w[h]);
+            const unsigned char* sp = kc + U::CODES + r * (DH / 16);
+            if constexpr (DH == 128)
+              sb[h] = *reinterpret_cast<const unsigned short*>(sp + 2 * t);
+            else
+              sb[h] = sp[DH == 64 ? t : t >> 1];
+            if (edge && (gone || r >= behind)) sb[h] = 0;  // no token there: bytes of any kind
           }
-          // the rows' sums, of the weights as O takes them: a product with ones
+          if (!WIDE) top_scale = max(top_scale, DH == 128 ? max(max(sb[0] & 255u, sb[1] & 255u), max(sb[0], sb[1]) >> 8)
+                                                          : max(sb[0], sb[1]));
+          Scale sc[2];
 #pragma unroll
-          for (int e = 0; e < TERMS; ++e)
-            mma(l[j], 0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u, pb[mt][j][e][0], pb[mt][j][e][1]);
-        }
-      // O^T += V^T P^T: keys 2t, 2t + 1, 2t + 8, 2t + 9 of a tile sit at rows t, t + 4, t + 8, t + 12
-      const unsigned char* const vc = kc + U::V_OFF;
+          for (int i = 0; i < WK; ++i) {
+            if (i == 0 || (DH == 128 && i == 2)) {
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        constexpr int WV = DH == 128 ? 2 : 1;
-        uint32_t w[4][WV], sb[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int r = 16 * mt + t + 4 * k;
-          if constexpr (DH == 32)
-            w[k][0] = *reinterpret_cast<const unsigned short*>(vc + r * (DH / 2) + 2 * g);
-          else
-            lds_words<WV>(vc + r * (DH / 2) + g * (DH / 16), w[k]);
-          sb[k] = vc[U::CODES + r * (DH / 16) + (DH == 128 ? g : DH == 64 ? g >> 1 : g >> 2)];
-          if (edge && (gone || r >= behind)) sb[k] = 0;  // no token there: bytes of any kind
-        }
-        const Scale sa = scale_pair((sb[0] + sb[1] * 0x10000u) * 128u),
-                    sz = scale_pair((sb[2] + sb[3] * 0x10000u) * 128u);
-#pragma unroll
-        for (int i = 0; i < WV; ++i)
-#pragma unroll
-          for (int half = 0; half < (DH == 32 ? 1 : 2); ++half) {
-            const uint32_t sel = half ? 0x7632u : 0x5410u;  // channels 4 half .. of both keys
+              for (int h = 0; h < 2; ++h) {
+                const uint32_t b = DH == 128 ? (i == 0 ? sb[h] & 255u : sb[h] >> 8) : sb[h];
+                sc[h] = scale_pair<WIDE>(b * 0x800080u);
+              }
+            }
             uint32_t v0[4], v1[4];
-            dequant(__byte_perm(w[0][i], w[1][i], sel), sa, v0);
-            dequant(__byte_perm(w[2][i], w[3][i], sel), sz, v1);
-            const int mu = 4 * i + 2 * half;
+            dequant<WIDE>(w[0][i], sc[0], v0);
+            dequant<WIDE>(w[1][i], sc[1], v1);
 #pragma unroll
             for (int j = 0; j < NT; ++j)
 #pragma unroll
               for (int e = 0; e < TERMS; ++e) {
-                mma(o[j][mu], v0[0], v0[1], v1[0], v1[1], pb[mt][j][e][0], pb[mt][j][e][1]);
-                mma(o[j][mu + 1], v0[2], v0[3], v1[2], v1[3], pb[mt][j][e][0], pb[mt][j][e][1]);
+                mma(s[mt][j], v0[0], v1[0], v0[1], v1[1], q[j][e][2 * i][0], q[j][e][2 * i][1]);
+                mma(s[mt][j], v0[2], v1[2], v0[3], v1[3], q[j][e][2 * i + 1][0], q[j][e][2 * i + 1][1]);
               }
           }
+        }
+        if (edge) {
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int key = key0 + 16 * mt + rk + 8 * (i >> 1), p = pos[j][i & 1];
+                if (gone || key > p || (p - key >= a.span.window && key >= a.span.sinks)) s[mt][j][i] = -INFINITY;
+              }
+        }
+        // The rows' references are raised only when some score passes one by more than 2^8: most units
+        // need no exchange between lanes and leave O as it is. Weights are 2^7 .. 2^15 at most.
+        bool above = false;
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            mx[j][c] = fmaxf(s[0][j][c], s[0][j][c + 2]);
+#pragma unroll
+            for (int mt = 1; mt < MT; ++mt) mx[j][c] = max3(mx[j][c], s[mt][j][c], s[mt][j][c + 2]);
+            above |= (mx[j][c] - m[j][c]) * rs[j][c] > 8.f;  // -inf less -inf: no
+          }
+        if (__any_sync(0xffffffffu, above)) {
+          far = false;
+#pragma unroll
+          for (int j = 0; j < NT; ++j) {
+            float corr[2];
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              float top = mx[j][c];
+              top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+              top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+              top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+              top = fmaxf(top, m[j][c]);
+              const float ref = top == -INFINITY ? 0.f : top;  // nothing seen yet: weights 2^-inf = 0
+              corr[c] = ex2((m[j][c] - ref) * rs[j][c]);
+              m[j][c] = top;
+              // s * rs - ref * rs in one rounding is off by 2^-24 of ref * rs: where that is large the
+              // difference is taken first
+              const bool big = fabsf(ref * rs[j][c]) > 1048576.f;
+              far |= big;
+              less[j][c] = big ? ref : 0.f;
+              off[j][c] = big ? 7.f : 7.f - ref * rs[j][c];
+            }
+#pragma unroll
+            for (int i = 0; i < MU; ++i) {
+              o[j][i][0] *= corr[0], o[j][i][1] *= corr[1];
+              o[j][i][2] *= corr[0], o[j][i][3] *= corr[1];
+            }
+            l[j][0] *= corr[0], l[j][1] *= corr[1];
+          }
+          far = __any_sync(0xffffffffu, far);
+        }
+        if (far) {
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) s[mt][j][i] -= less[j][i & 1];
+        }
+        uint32_t pb[MT][NT][TERMS][2];
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              fma_pair(s[mt][j][2 * h], s[mt][j][2 * h + 1], rs[j][0], rs[j][1], off[j][0], off[j][1]);
+              const float p0 = ex2(s[mt][j][2 * h]), p1 = ex2(s[mt][j][2 * h + 1]);
+              pb[mt][j][0][h] = transpose8(pack2<__half>(p0, p1));
+              if constexpr (SPLIT) pb[mt][j][1][h] = transpose8(pack2<__half>(lo_term<__half>(p0), lo_term<__half>(p1)));
+            }
+            // the rows' sums, of the weights as O takes them: a product with ones
+#pragma unroll
+            for (int e = 0; e < TERMS; ++e)
+              mma(l[j], 0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u, pb[mt][j][e][0], pb[mt][j][e][1]);
+          }
+        // O^T += V^T P^T: keys 2t, 2t + 1, 2t + 8, 2t + 9 of a tile sit at rows t, t + 4, t + 8, t + 12
+        const unsigned char* const vc = kc + U::V_OFF;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          constexpr int WV = DH == 128 ? 2 : 1;
+          uint32_t w[4][WV], sb[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int r = 16 * mt + t + 4 * k;
+            if constexpr (DH == 32)
+              w[k][0] = *reinterpret_cast<const unsigned short*>(vc + r * (DH / 2) + 2 * g);
+            else
+              lds_words<WV>(vc + r * (DH / 2) + g * (DH / 16), w[k]);
+            sb[k] = vc[U::CODES + r * (DH / 16) + (DH == 128 ? g : DH == 64 ? g >> 1 : g >> 2)];
+            if (edge && (gone || r >= behind)) sb[k] = 0;  // no token there: bytes of any kind
+          }
+          const Scale sa = scale_pair<WIDE>((sb[0] + sb[1] * 0x10000u) * 128u),
+                      sz = scale_pair<WIDE>((sb[2] + sb[3] * 0x10000u) * 128u);
+#pragma unroll
+          for (int i = 0; i < WV; ++i)
+#pragma unroll
+            for (int half = 0; half < (DH == 32 ? 1 : 2); ++half) {
+              const uint32_t sel = half ? 0x7632u : 0x5410u;  // channels 4 half .. of both keys
+              uint32_t v0[4], v1[4];
+              dequant<WIDE>(__byte_perm(w[0][i], w[1][i], sel), sa, v0);
+              dequant<WIDE>(__byte_perm(w[2][i], w[3][i], sel), sz, v1);
+              const int mu = 4 * i + 2 * half;
+#pragma unroll
+              for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int e = 0; e < TERMS; ++e) {
+                  mma(o[j][mu], v0[0], v0[1], v1[0], v1[1], pb[mt][j][e][0], pb[mt][j][e][1]);
+                  mma(o[j][mu + 1], v0[2], v0[3], v1[2], v1[3], pb[mt][j][e][0], pb[mt][j][e][1]);
+                }
+            }
+        }
+        __syncwarp();  // every lane has read the stage
+        if (++st_out == kStages) {
+          st_out = 0;
+          ph_out ^= 1u;
+        }
+        if (i + kStages < count) copy(i + kStages);
       }
-      __syncwarp();  // every lane has read the stage
-      if (++st_out == kStages) {
-        st_out = 0;
-        ph_out ^= 1u;
-      }
-      if (i + kStages < count) copy(i + kStages);
+    };
+    clear();
+    pass(std::false_type{});
+    // A scale that is too large for the short way: keys' are looked at, values' show in O. Once more
+    // then, the long way (as for a query that is not finite, to no effect).
+    bool again = top_scale >= kWideScale;
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int i = 0; i < MU; ++i)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) again |= !(fabsf(o[j][i][k]) <= 3.4028235e38f);
+    if (__any_sync(0xffffffffu, again)) {
+      clear();
+      for (int i = 0; i < min(kStages, count); ++i) copy(i);
+      pass(std::true_type{});
     }
 #pragma unroll
     for (int j = 0; j < NT; ++j)

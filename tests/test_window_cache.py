@@ -295,6 +295,33 @@ def test_cache_attention_of_large_and_small_numbers(cuda_ok, dtype):
 
 
 @gpu
+@pytest.mark.parametrize("dtype,dh", [("bf16", 64), ("f32", 64), ("bf16", 128), ("f32", 32)])
+@pytest.mark.parametrize("which", ["keys", "values"])
+def test_cache_attention_of_the_largest_and_smallest_scales(cuda_ok, dtype, dh, which):
+    """Blocks up to the format's ends (scales 8192 and 9216, 2^-17), of both signs, in one of 2000 tokens."""
+    H, Hkv, T = 4, 1, 2000
+    for size in (6.4e4, 3e4, 1e-4, 6e-5):
+        s = Setup([T], Hkv, dh)
+        kv = [normal(i, (1, T, dh), "f32") for i in (1, 2)]
+        x = kv[which == "values"]
+        if size > 1:
+            x[0, 1234] *= size / x[0, 1234].abs().max()
+        else:
+            x *= size / 3
+        rmt.rmt_cache_write(s.cache, *kv, T, dtype="f32")
+        q = normal(4, (1, 1, H * dh), dtype)
+        if which == "keys":
+            q = (q.float() * (3.0 / size)).to(TORCH[dtype])
+        out = f64(s.attend(q, 1, H, 0, 0, dtype))
+        rmt.rmt_sync(None)
+        (k, v), = s.values()
+        if size > 1 and which == "values":
+            assert s.halves()[3].max() == 0xFF and np.abs(v).max() >= 0.9 * size
+        ref = attend_ref(f64(q)[0].reshape(1, H, dh), k, v, np.array([T - 1]), 0, 0)
+        check_attention(out[0].reshape(1, H, dh), ref, np.abs(v).max(), dtype)
+
+
+@gpu
 def test_cache_attention_of_queries_that_are_not_finite(cuda_ok):
     s = Setup([100], 1, 64)
     s.fill(1)
