@@ -160,8 +160,15 @@ DeviceScratch g_dev_scratch[64];
 __device__ int g_err_word;
 
 rmt_status current_error_word(int** err) {
-  void* p = nullptr;
-  RMT_CUDA(cudaGetSymbolAddress(&p, g_err_word));
+  static std::atomic<void*> known[64];  // per device; threads that race here store the same address
+  int dev = 0;
+  RMT_CUDA(cudaGetDevice(&dev));
+  if (dev < 0 || dev >= 64) return fail(RMT_EINVAL, "device index out of range");
+  void* p = known[dev].load(std::memory_order_acquire);
+  if (!p) {
+    RMT_CUDA(cudaGetSymbolAddress(&p, g_err_word));
+    known[dev].store(p, std::memory_order_release);
+  }
   *err = static_cast<int*>(p);
   return RMT_OK;
 }

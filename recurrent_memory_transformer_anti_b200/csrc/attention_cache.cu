@@ -4,8 +4,9 @@
 // work is 64 tokens of one kv head (32 at head_dim 128: 4608 bytes either way) for one tile of query
 // rows; an item is what one (sequence, kv head, row tile) sees of the cache, without what lies between
 // the sinks and the window. Two ways of dealing the units, by the most units an item can have:
-//   up to kWholeUnits: a CTA takes whole items, its eight warps every eighth unit, and adds
-//     their results in shared memory: one launch, nothing read before the item's own length.
+//   up to kWholeUnits: a team of warps takes whole items, each warp every so-manieth unit, and adds
+//     their results in shared memory: one launch, nothing read before the item's own length. A
+//     team has as many warps of a CTA as leave every item a team at once, at most one per unit.
 //   more: the units of all items form one list (lengths are read on the device), and each warp
 //     of the grid takes an equal, contiguous stretch of it, so that one long sequence and many short
 //     ones are both spread over all SMs, and no warp waits for another. A stretch that holds a whole
@@ -76,6 +77,7 @@ struct DecodeArgs {
   long long ldq;
   void* out;
   int n_q, H, group, rows, tiles;  // rows: n_q * group per kv head, in `tiles` tiles
+  int team;       // warps that share an item (whole items)
   int* prefix;    // [n_seqs + 1] units before each sequence (workspace; for the second kernel)
   float* parts;   // two per warp: O [rows of a tile][dh], maxima, sums
 };
@@ -326,14 +328,15 @@ __global__ void __launch_bounds__(32 * Shape<DH, NT>::WARPS, 1) cache_attn_kerne
   uint32_t ph_out = 0;
   unsigned bad = 0;          // bit per stage: no such page, the unit's keys are masked
   const int items = n * per_seq;
-  for (int at = WHOLE ? static_cast<int>(blockIdx.x) : r0; at < (WHOLE ? items : r1);) {
+  const int team = WHOLE ? a.team : 1, my_team = warp / team, in_team = warp - my_team * team;
+  for (int at = WHOLE ? static_cast<int>(blockIdx.x + gridDim.x * my_team) : r0; at < (WHOLE ? items : r1);) {
     const Item x = item_at(at);
     // this warp's units of the item: k0, k0 + step, .. (count of them)
-    const int step = WHOLE ? kWarps : 1;
-    const int k0 = WHOLE ? warp : at - x.begin;
+    const int step = team;
+    const int k0 = WHOLE ? in_team : at - x.begin;
     const int k1 = WHOLE ? x.s.n : min(x.s.n, r1 - x.begin);
     const int count = max(0, (k1 - k0 + step - 1) / step);
-    if (WHOLE && x.head == 0 && x.tile == 0 && threadIdx.x == 0 && a.c.err && x.len > a.span.cap)
+    if (WHOLE && x.head == 0 && x.tile == 0 && in_team == 0 && lane == 0 && a.c.err && x.len > a.span.cap)
       atomicOr(a.c.err, kErrPage);
     const unsigned char* const head_base = a.c.pages + static_cast<size_t>(x.head) * cache4::Layout<DH>::BLOCK;
     const int* const table = a.c.table + static_cast<size_t>(x.b) * a.c.max_pages;
@@ -651,6 +654,15 @@ __global__ void __launch_bounds__(32 * Shape<DH, NT>::WARPS, 1) cache_attn_kerne
     };
     if constexpr (WHOLE) {
       // the warps' results of the item, added
+      const int w0 = my_team * team;
+      auto meet = [&]() {
+        if (team == kWarps)
+          __syncthreads();
+        else if (team > 1)
+          asm volatile("bar.sync %0, %1;" ::"r"(1 + my_team), "r"(32 * team) : "memory");
+        else
+          __syncwarp();
+      };
       float* const merge = reinterpret_cast<float*>(smem + S::MERGE);
       float* const ml = reinterpret_cast<float*>(smem + S::ML);
 #pragma unroll
@@ -663,29 +675,27 @@ __global__ void __launch_bounds__(32 * Shape<DH, NT>::WARPS, 1) cache_attn_kerne
           }
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
-        __syncthreads();
+        meet();
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           float top = -INFINITY;
-#pragma unroll
-          for (int w = 0; w < kWarps; ++w) top = fmaxf(top, ml[w * 8 * NT + 8 * j + 2 * t + c]);
+          for (int w = w0; w < w0 + team; ++w) top = fmaxf(top, ml[w * 8 * NT + 8 * j + 2 * t + c]);
           const float by = top == -INFINITY && m[j][c] == top ? (l[j][c] == l[j][c] ? 0.f : NAN) : ex2(m[j][c] - top);
 #pragma unroll
           for (int i = 0; i < MU; ++i)
             *reinterpret_cast<float2*>(merge + (warp * 8 + 2 * t + c) * S::LD + g * (DH / 8) + 2 * i) =
                 make_float2(o[j][i][c] * by, o[j][i][c + 2] * by);
         }
-        __syncthreads();
-        for (int e = threadIdx.x; e < 8 * DH / 4; e += kThreads) {
+        meet();
+        for (int e = 32 * in_team + lane; e < 8 * DH / 4; e += 32 * team) {
           const int row = e / (DH / 4), ch = (e - row * (DH / 4)) * 4;
           const int rr = (x.tile * NT + j) * 8 + row;
           if (rr >= a.rows) continue;
           float top = -INFINITY, sum = 0.f;
-#pragma unroll
-          for (int w = 0; w < kWarps; ++w) top = fmaxf(top, ml[w * 8 * NT + 8 * j + row]);
+          for (int w = w0; w < w0 + team; ++w) top = fmaxf(top, ml[w * 8 * NT + 8 * j + row]);
           float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-          for (int w = 0; w < kWarps; ++w) {
+#pragma unroll 4
+          for (int w = w0; w < w0 + team; ++w) {
             const float lw = ml[(kWarps + w) * 8 * NT + 8 * j + row], mw = ml[w * 8 * NT + 8 * j + row];
             sum += mw == -INFINITY ? lw * 0.f : lw * ex2(mw - top);  // 0, or NaN of a query that is not finite
             const float4 v = *reinterpret_cast<const float4*>(merge + (w * 8 + row) * S::LD + ch);
@@ -700,8 +710,8 @@ __global__ void __launch_bounds__(32 * Shape<DH, NT>::WARPS, 1) cache_attn_kerne
                 make_uint2(pack2<T>(acc.x * inv, acc.y * inv), pack2<T>(acc.z * inv, acc.w * inv));
         }
       }
-      __syncthreads();  // ml and merge may be written again
-      at += gridDim.x;
+      meet();  // ml and merge may be written again
+      at += gridDim.x * (kWarps / team);
     } else {
       const bool all = k0 == 0 && k1 == x.s.n;
       float* const part = a.parts + static_cast<size_t>(2 * wid + (at == r0 ? 0 : 1)) * (DH + 2) * 8 * NT;
@@ -838,6 +848,7 @@ struct Plan {
   bool whole;
   long long items, units;
   int ctas, warps;  // warps: of the grid, when they share a list of units
+  int team;
 };
 Plan plan_of(int n_seqs, int max_pages, int n_q, int tiles, int Hkv, int dh, int window, int sinks,
              int cta_warps) {
@@ -846,10 +857,12 @@ Plan plan_of(int n_seqs, int max_pages, int n_q, int tiles, int Hkv, int dh, int
   p.items = static_cast<long long>(n_seqs) * Hkv * tiles;
   p.units = p.items * most;
   p.whole = most <= kWholeUnits;
-  const long long cap = 148;  // one per SM
-  const long long want =
-      p.whole ? p.items : (p.units + static_cast<long long>(cta_warps) * kLeastUnits - 1) / (cta_warps * kLeastUnits);
-  p.ctas = static_cast<int>(want < cap ? want : cap);
+  // the widest team that leaves every item one at once (148 SMs)
+  p.team = cta_warps;
+  while (p.team > 1 && (cta_warps % p.team || p.team > most || p.items * p.team > 148LL * cta_warps)) --p.team;
+  const long long share = p.whole ? cta_warps / p.team : cta_warps * kLeastUnits;
+  const long long want = ((p.whole ? p.items : p.units) + share - 1) / share;
+  p.ctas = static_cast<int>(want < 148 ? want : 148);  // one per SM
   p.warps = p.ctas * cta_warps;
   return p;
 }
@@ -867,8 +880,10 @@ cudaError_t launch_decode(const CacheAttnArgs& c, cudaStream_t st) {
   const Plan p = plan_of(c.c.n_seqs, c.c.max_pages, c.n_q, a.tiles, c.c.Hkv, DH, c.window, c.sinks, kWarps);
   auto kernel = p.whole ? cache_attn_kernel<DH, T, NT, true> : cache_attn_kernel<DH, T, NT, false>;
   const int smem = p.whole ? DecodeSmem<DH, NT, true>::BYTES : DecodeSmem<DH, NT, false>::BYTES;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static std::atomic<uint64_t> done[2];
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), smem, done[p.whole]);
   if (e != cudaSuccess) return e;
+  a.team = p.team;
   if (!p.whole) {
     a.parts = static_cast<float*>(c.ws);
     a.prefix = reinterpret_cast<int*>(a.parts + static_cast<size_t>(2) * p.warps * (DH + 2) * 8 * NT);

@@ -190,8 +190,8 @@ __global__ void __launch_bounds__(128) window_simt_kernel(const WindowAttnArgs a
 template <int DH, typename T>
 cudaError_t launch_simt(const WindowAttnArgs& a, cudaStream_t st) {
   using S = WinSimt<DH>;
-  cudaError_t e =
-      cudaFuncSetAttribute(window_simt_kernel<DH, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::BYTES);
+  static std::atomic<uint64_t> done;
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(window_simt_kernel<DH, T>), S::BYTES, done);
   if (e != cudaSuccess) return e;
   const dim3 grid((a.M + S::BQ - 1) / S::BQ, a.H, a.G);
   e = launch_pdl(window_simt_kernel<DH, T>, grid, dim3(128), S::BYTES, st, a);

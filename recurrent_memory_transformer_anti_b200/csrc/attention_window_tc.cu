@@ -626,13 +626,10 @@ cudaError_t launch_hd(const WindowAttnArgs& w, cudaStream_t st) {
   if (!make_tmap_bf16_3d(&maps.q, w.qkv, inner, w.M, w.G, a.tq)) return cudaErrorInvalidValue;
   for (int i = 0; i < 5; ++i)
     if (!make_tmap_bf16_3d(&maps.kv[i], w.qkv, inner, w.M, w.G, 128u >> i)) return cudaErrorInvalidValue;
-  int dev = 0, sms = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(window_tc_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  static std::atomic<uint64_t> done;
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(window_tc_kernel<HD>), C::SMEM, done);
   if (e != cudaSuccess) return e;
-  const int grid = a.items < sms ? a.items : sms;
+  const int grid = a.items < 148 ? a.items : 148;  // one CTA per SM
   e = launch_pdl(window_tc_kernel<HD>, dim3(grid), dim3(384), C::SMEM, st, maps, a);
   return e != cudaSuccess ? e : cudaGetLastError();
 }

@@ -167,24 +167,38 @@ def _ptr32(x):
 def _rows(x, n: int, M: int, width: int, dtype: str):
     """Address and row stride (elements) of n * M rows of `width` values: a tensor [n, M, ...] whose rows
     are contiguous and equally spaced, possibly a slice of wider rows."""
-    if dtype not in ("f32", "bf16") or ("bfloat16" if dtype == "bf16" else "float32") not in str(x.dtype):
+    if _ROW_TYPES.get(str(x.dtype)) != dtype:
         raise TypeError(f"rows of type {x.dtype} given as {dtype!r}")
-    shape, st = tuple(x.shape), x.stride()
-    if x.ndim < 3 or shape[:2] != (n, M) or x.numel() != n * M * width:
-        raise ValueError(f"rows must be [{n}, {M}, {width}], not {shape}")
+    shape, st = x.shape, x.stride()
+    if len(shape) < 3 or shape[0] != n or shape[1] != M or x.numel() != n * M * width:
+        raise ValueError(f"rows must be [{n}, {M}, {width}], not {tuple(shape)}")
     ld = st[1] if M > 1 else st[0] if n > 1 else width
-    inner = [1]
-    for s in reversed(shape[3:]):
-        inner.insert(0, inner[0] * s)
-    if ld < width or (n > 1 and st[0] != M * ld) or any(a != b for a, b, s in zip(st[2:], inner, shape[2:]) if s > 1):
+    ok = ld >= width and (n == 1 or st[0] == M * ld)
+    step = 1
+    for d in range(len(shape) - 1, 1, -1):
+        ok = ok and (shape[d] == 1 or st[d] == step)
+        step *= shape[d]
+    if not ok:
         raise ValueError("rows must be contiguous and equally spaced")
     return x.data_ptr(), ld
 
 
+_ROW_TYPES = {"torch.bfloat16": "bf16", "torch.float32": "f32"}
+
+
+_current_stream = None  # () -> the raw current stream, once CUDA was found available
+
+
 def _stream(stream):
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream if torch.cuda.is_available() else None
+        global _current_stream
+        if _current_stream is None:
+            import torch
+            if not torch.cuda.is_available():
+                return None
+            raw, device = getattr(torch._C, "_cuda_getCurrentRawStream", None), torch.cuda.current_device
+            _current_stream = (lambda: raw(device())) if raw else (lambda: torch.cuda.current_stream().cuda_stream)
+        return _current_stream()
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
@@ -380,6 +394,9 @@ class Cache:
     def __init__(self, struct: rmt_cache_struct, keep: tuple):
         self.struct = struct
         self.keep = keep
+        self.ref = ctypes.byref(struct)
+        self.n_seqs, self.head_dim = struct.n_seqs, struct.head_dim
+        self.width = struct.n_kv_heads * struct.head_dim
 
 
 def rmt_cache_page_bytes(n_kv_heads: int, head_dim: int) -> int:
@@ -401,28 +418,26 @@ def rmt_cache(pages, page_table, lens, n_kv_heads: int, head_dim: int) -> Cache:
     return Cache(s, (pages, page_table, lens))
 
 
-def rmt_cache_write(cache: Cache, k, v, M, n_new=None, dtype="bf16", stream=None) -> None:
-    """Quantise rows k, v ([n_seqs, M, n_kv_heads * head_dim], views into wider rows allowed) into the cache."""
-    width = cache.struct.n_kv_heads * cache.struct.head_dim
-    (pk, ld), (pv, ldv) = (_rows(x, cache.struct.n_seqs, M, width, dtype) for x in (k, v))
+def _cache_rows(fn, name, cache, k, v, M, n_new, dtype, stream):
+    pk, ld = _rows(k, cache.n_seqs, M, cache.width, dtype)
+    pv, ldv = _rows(v, cache.n_seqs, M, cache.width, dtype)
     if ld != ldv:
         raise ValueError("k and v need the same row stride")
-    _check(_lib.rmt_cache_write(ctypes.byref(cache.struct), pk, pv, ld, M, _ptr32(n_new), DTYPES[dtype],
-                                _stream(stream)), "rmt_cache_write")
+    _check(fn(cache.ref, pk, pv, ld, M, _ptr32(n_new), DTYPES[dtype], _stream(stream)), name)
+
+
+def rmt_cache_write(cache: Cache, k, v, M, n_new=None, dtype="bf16", stream=None) -> None:
+    """Quantise rows k, v ([n_seqs, M, n_kv_heads * head_dim], views into wider rows allowed) into the cache."""
+    _cache_rows(_lib.rmt_cache_write, "rmt_cache_write", cache, k, v, M, n_new, dtype, stream)
 
 
 def rmt_cache_read(cache: Cache, k, v, M, n_new=None, dtype="bf16", stream=None) -> None:
     """The values the cache holds for the rows rmt_cache_write takes, into k, v."""
-    width = cache.struct.n_kv_heads * cache.struct.head_dim
-    (pk, ld), (pv, ldv) = (_rows(x, cache.struct.n_seqs, M, width, dtype) for x in (k, v))
-    if ld != ldv:
-        raise ValueError("k and v need the same row stride")
-    _check(_lib.rmt_cache_read(ctypes.byref(cache.struct), pk, pv, ld, M, _ptr32(n_new), DTYPES[dtype],
-                               _stream(stream)), "rmt_cache_read")
+    _cache_rows(_lib.rmt_cache_read, "rmt_cache_read", cache, k, v, M, n_new, dtype, stream)
 
 
 def rmt_attention_cache_workspace(cache: Cache, n_q: int, H: int, window: int = 0, sinks: int = 0) -> int:
-    n = _lib.rmt_attention_cache_workspace(ctypes.byref(cache.struct), n_q, H, window, sinks)
+    n = _lib.rmt_attention_cache_workspace(cache.ref, n_q, H, window, sinks)
     if n == 0:
         raise RmtError(RMT_EINVAL, "rmt_attention_cache_workspace", rmt_last_error())
     return n
@@ -431,8 +446,8 @@ def rmt_attention_cache_workspace(cache: Cache, n_q: int, H: int, window: int = 
 def rmt_attention_cache(cache: Cache, q, out, n_q, H, window, sinks, workspace, dtype="bf16", stream=None) -> None:
     """Attention of the newest n_q tokens of each sequence (q rows [n_seqs, n_q, H * head_dim], a view into
     wider rows allowed) over the cache. workspace: a uint8 tensor of rmt_attention_cache_workspace bytes."""
-    pq, ldq = _rows(q, cache.struct.n_seqs, n_q, H * cache.struct.head_dim, dtype)
-    _check(_lib.rmt_attention_cache(ctypes.byref(cache.struct), pq, ldq, _ptr(out), n_q, H, window, sinks,
+    pq, ldq = _rows(q, cache.n_seqs, n_q, H * cache.head_dim, dtype)
+    _check(_lib.rmt_attention_cache(cache.ref, pq, ldq, _ptr(out), n_q, H, window, sinks,
                                     _ptr(workspace), workspace.numel() * workspace.element_size(), DTYPES[dtype],
                                     _stream(stream)), "rmt_attention_cache")
 
