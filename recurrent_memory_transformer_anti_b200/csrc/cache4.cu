@@ -1,7 +1,13 @@
 // Writing rows into the 4-bit key/value cache, and reading them back (layout and arithmetic:
 // cache4.cuh). Both stream: one thread holds the 16 channels of one scale, so a block's maximum
 // needs no other lane, and a warp covers 512 channels of one head's keys or values -- 16, 8 or 4
-// tokens -- so that its codes and its scales each land in whole 32-byte sectors.
+// tokens -- so that its codes and its scales each land in whole 32-byte sectors. A warp takes four
+// such (keys or values, head) columns of its tokens where there are warps enough, with their loads in
+// flight together and the tokens' pages looked up once.
+//
+// Bound by HBM if the arithmetic stays at about 5 instructions a channel: a bf16 channel is
+// rounded in two (encode_short); blocks with a NaN, a saturating value or a scale below 2^-14, and fp32,
+// take the general way (encode_value).
 #include "cache4.cuh"
 #include "launch.h"
 
@@ -10,92 +16,48 @@ namespace {
 
 using cache4::kPage;
 
-// 16 consecutive values of a row
-__device__ __forceinline__ void load16(const float* p, float (&x)[16]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float4 f = __ldcs(reinterpret_cast<const float4*>(p) + i);
-    x[4 * i] = f.x, x[4 * i + 1] = f.y, x[4 * i + 2] = f.z, x[4 * i + 3] = f.w;
-  }
-}
-__device__ __forceinline__ void load16(const __nv_bfloat16* p, float (&x)[16]) {
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const uint4 u = __ldcs(reinterpret_cast<const uint4*>(p) + i);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      x[8 * i + 2 * j] = __uint_as_float(w[j] << 16);
-      x[8 * i + 2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
-    }
-  }
-}
-__device__ __forceinline__ void store16(float* p, const float (&x)[16]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    __stcs(reinterpret_cast<float4*>(p) + i, make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]));
-}
-__device__ __forceinline__ void store16(__nv_bfloat16* p, const float (&x)[16]) {
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-    __stcs(reinterpret_cast<uint4*>(p) + i,
-           make_uint4(pack_bf16(x[8 * i], x[8 * i + 1]), pack_bf16(x[8 * i + 2], x[8 * i + 3]),
-                      pack_bf16(x[8 * i + 4], x[8 * i + 5]), pack_bf16(x[8 * i + 6], x[8 * i + 7])));
-}
-
-// The 16 channels of this thread: which token, which of the head's blocks, where in the cache.
+// Where this thread's token is: its row of k and v, and its page.
 struct Spot {
-  long long row;  // row of k, v; -1: nothing to do
-  int head, blk;
-  bool value;
-  unsigned char* block;  // the (page, kv head) block
+  bool on;
+  size_t row;
+  unsigned char* page;
   int in_page;
 };
 
 template <int DH>
-__device__ __forceinline__ Spot find_spot(const CacheRowsArgs& a) {
-  constexpr int BLK = DH / cache4::kBlock, TOK = 32 / BLK;
-  Spot s;
-  const long long warp = (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
-  const int lane = threadIdx.x & 31;
-  const int cols = 2 * a.c.Hkv;  // (keys or values, head) of a group of tokens
-  const long long group = warp / cols;
-  const int col = static_cast<int>(warp - group * cols);
-  s.value = col >= a.c.Hkv;
-  s.head = col - (s.value ? a.c.Hkv : 0);
-  s.blk = lane % BLK;
-  s.row = group * TOK + lane / BLK;
-  if (s.row >= static_cast<long long>(a.c.n_seqs) * a.M) {
-    s.row = -1;
-    return s;
-  }
-  const int b = static_cast<int>(s.row / a.M), i = static_cast<int>(s.row - static_cast<long long>(b) * a.M);
+__device__ __forceinline__ Spot find_spot(const CacheRowsArgs& a, unsigned group) {
+  constexpr unsigned BLK = DH / cache4::kBlock, TOK = 32 / BLK;
+  Spot s{};
+  const unsigned row = group * TOK + (threadIdx.x & 31u) / BLK;
+  if (row >= static_cast<unsigned>(a.c.n_seqs) * a.M) return s;
+  const unsigned b = row / static_cast<unsigned>(a.M), i = row - b * a.M;
   const int n = a.n_new ? min(__ldg(a.n_new + b), a.M) : a.M;
-  const int pos = __ldg(a.c.lens + b) - n + i;
-  if (i >= n || pos < 0) {  // a row past the sequence's new ones, or of an empty slot
-    s.row = -1;
-    return s;
-  }
+  const int pos = __ldg(a.c.lens + b) - n + static_cast<int>(i);
+  if (static_cast<int>(i) >= n || pos < 0) return s;  // past the sequence's new rows, or of an empty slot
   const int page = cache4::page_of(a.c, b, pos);
-  if (page < 0) {
-    s.row = -1;
-    return s;
-  }
-  s.block = a.c.pages + cache4::block_offset<DH>(a.c, page, s.head);
+  if (page < 0) return s;
+  s.on = true;
+  s.row = row;
+  s.page = a.c.pages + cache4::block_offset<DH>(a.c, page, 0);
   s.in_page = pos % kPage;
   return s;
 }
 
-template <int DH, typename T>
-__global__ void __launch_bounds__(256) cache_write_kernel(const CacheRowsArgs a) {
-  pdl_trigger();
-  pdl_wait();
-  using L = cache4::Layout<DH>;
-  const Spot s = find_spot<DH>(a);
-  if (s.row < 0) return;
-  const T* src = static_cast<const T*>(s.value ? a.v : a.k) + s.row * a.ld + s.head * DH + s.blk * cache4::kBlock;
-  float x[16];
-  load16(src, x);
+// 16 consecutive values of a row, as loaded
+template <typename T>
+struct Raw {
+  uint4 v[sizeof(T)];
+};
+template <typename T>
+__device__ __forceinline__ Raw<T> load16(const T* p) {
+  Raw<T> r;
+#pragma unroll
+  for (int i = 0; i < static_cast<int>(sizeof(T)); ++i) r.v[i] = __ldcs(reinterpret_cast<const uint4*>(p) + i);
+  return r;
+}
+
+// Their scale byte and codes
+__device__ __forceinline__ uint32_t encode_general(float (&x)[16], uint32_t& lo, uint32_t& hi) {
   float amax = 0.f;
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
@@ -103,7 +65,7 @@ __global__ void __launch_bounds__(256) cache_write_kernel(const CacheRowsArgs a)
     amax = fmaxf(amax, fabsf(x[i]));
   }
   const uint32_t sb = cache4::encode_scale(amax);
-  uint32_t lo = 0x88888888u, hi = 0x88888888u;  // a block of zeros
+  lo = hi = 0x88888888u;  // a block of zeros
   if (sb) {
     const float sc = cache4::decode_scale(sb), rs = 1.f / sc;
     lo = hi = 0;
@@ -113,41 +75,157 @@ __global__ void __launch_bounds__(256) cache_write_kernel(const CacheRowsArgs a)
       hi |= cache4::encode_value(x[8 + i], sc, rs) << (4 * i);
     }
   }
-  unsigned char* half = s.block + (s.value ? L::V_OFF : 0);
-  *reinterpret_cast<uint2*>(half + s.in_page * L::CODE_ROW + s.blk * 8) = make_uint2(lo, hi);
-  half[L::CODES + s.in_page * L::SCALE_ROW + s.blk] = static_cast<unsigned char>(sb);
+  return sb;
 }
-
-template <int DH, typename T>
-__global__ void __launch_bounds__(256) cache_read_kernel(const CacheRowsArgs a) {
-  pdl_trigger();
-  pdl_wait();
-  using L = cache4::Layout<DH>;
-  const Spot s = find_spot<DH>(a);
-  if (s.row < 0) return;
-  const unsigned char* half = s.block + (s.value ? L::V_OFF : 0);
-  const uint2 w = *reinterpret_cast<const uint2*>(half + s.in_page * L::CODE_ROW + s.blk * 8);
-  const float sc = cache4::decode_scale(half[L::CODES + s.in_page * L::SCALE_ROW + s.blk]);
+__device__ __forceinline__ uint32_t encode16(const Raw<float>& r, uint32_t& lo, uint32_t& hi) {
+  float x[16];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[4 * i] = __uint_as_float(r.v[i].x), x[4 * i + 1] = __uint_as_float(r.v[i].y);
+    x[4 * i + 2] = __uint_as_float(r.v[i].z), x[4 * i + 3] = __uint_as_float(r.v[i].w);
+  }
+  return encode_general(x, lo, hi);
+}
+__device__ __forceinline__ uint32_t encode16(const Raw<__nv_bfloat16>& r, uint32_t& lo, uint32_t& hi) {
+  const uint32_t w[8] = {r.v[0].x, r.v[0].y, r.v[0].z, r.v[0].w, r.v[1].x, r.v[1].y, r.v[1].z, r.v[1].w};
+  __nv_bfloat162 m = __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[0]));
+#pragma unroll
+  for (int i = 1; i < 8; ++i) m = __hmax2_nan(m, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[i])));
+  const float amax = __bfloat162float(__hmax_nan(m.x, m.y));
   float x[16];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    x[i] = static_cast<float>(static_cast<int>((w.x >> (4 * i)) & 15u) - 8) * sc;
-    x[8 + i] = static_cast<float>(static_cast<int>((w.y >> (4 * i)) & 15u) - 8) * sc;
+    x[2 * i] = __uint_as_float(w[i] << 16);
+    x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
   }
-  T* dst = static_cast<T*>(s.value ? a.v : a.k) + s.row * a.ld + s.head * DH + s.blk * cache4::kBlock;
-  store16(dst, x);
+  const uint32_t sb = cache4::encode_scale(amax);
+  // short way: scales from 2^-14 on (within 1/16 of max / 7, so quotients stay below 7.5), no
+  // saturation, no NaN
+  if (!(amax <= cache4::kAmax) || sb < 8) return encode_general(x, lo, hi);
+  const float rs = 1.f / cache4::decode_scale(sb);
+  uint32_t u[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) u[i] = cache4::encode_short(x[i], rs);
+  // low bytes: even channels, then odd ones in the high nibbles
+  auto bytes = [](uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
+  };
+  lo = bytes(u[0], u[2], u[4], u[6]) + 16u * bytes(u[1], u[3], u[5], u[7]);
+  hi = bytes(u[8], u[10], u[12], u[14]) + 16u * bytes(u[9], u[11], u[13], u[15]);
+  return sb;
+}
+
+// Columns col .. col + COLS - 1 of a token group: keys of heads 0 .. Hkv - 1, then values.
+template <int DH, typename T, int COLS>
+__global__ void __launch_bounds__(256) cache_write_kernel(const CacheRowsArgs a, unsigned cols) {
+  pdl_trigger();
+  pdl_wait();
+  using L = cache4::Layout<DH>;
+  const unsigned warp = (blockIdx.x * blockDim.x + threadIdx.x) >> 5;
+  const unsigned group = warp / cols, col = (warp - group * cols) * COLS;
+  const int blk = (threadIdx.x & 31) % (DH / cache4::kBlock);
+  const Spot s = find_spot<DH>(a, group);
+  if (!s.on) return;
+  Raw<T> raw[COLS];
+#pragma unroll
+  for (int c = 0; c < COLS; ++c) {
+    const bool value = col + c >= static_cast<unsigned>(a.c.Hkv);
+    const unsigned head = col + c - (value ? a.c.Hkv : 0);
+    raw[c] = load16(static_cast<const T*>(value ? a.v : a.k) + s.row * a.ld + head * DH + blk * cache4::kBlock);
+  }
+#pragma unroll
+  for (int c = 0; c < COLS; ++c) {
+    const bool value = col + c >= static_cast<unsigned>(a.c.Hkv);
+    const unsigned head = col + c - (value ? a.c.Hkv : 0);
+    uint32_t lo, hi;
+    const uint32_t sb = encode16(raw[c], lo, hi);
+    unsigned char* half = s.page + static_cast<size_t>(head) * L::BLOCK + (value ? L::V_OFF : 0);
+    *reinterpret_cast<uint2*>(half + s.in_page * L::CODE_ROW + blk * 8) = make_uint2(lo, hi);
+    half[L::CODES + s.in_page * L::SCALE_ROW + blk] = static_cast<unsigned char>(sb);
+  }
+}
+
+// 16 channels from their codes and scale byte. A nibble or-ed into the pattern of a power of two is that
+// plus q + 8; less that and 8, times the scale: exact.
+__device__ __forceinline__ void decode16(float* dst, uint2 w, uint32_t sb) {
+  const float sc = cache4::decode_scale(sb), less = -8388616.f * sc;  // exact: 2^20 + 1 times 8 scales
+  float x[16];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    x[i] = fmaf(__uint_as_float(((w.x >> (4 * i)) & 15u) | 0x4B000000u), sc, less);
+    x[8 + i] = fmaf(__uint_as_float(((w.y >> (4 * i)) & 15u) | 0x4B000000u), sc, less);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    __stcs(reinterpret_cast<float4*>(dst) + i, make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]));
+}
+__device__ __forceinline__ void decode16(__nv_bfloat16* dst, uint2 w, uint32_t sb) {
+  const __nv_bfloat162 sc = __float2bfloat162_rn(cache4::decode_scale(sb));  // 4 significant bits
+  const __nv_bfloat162 less = __float2bfloat162_rn(-136.f);                  // 128 + 8
+  uint32_t out[8];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t v[4];
+    const uint32_t u = h ? w.y : w.x;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {  // channels j and j + 4
+      const uint32_t n = ((u >> (4 * j)) & 0x000F000Fu) | 0x43004300u;
+      const __nv_bfloat162 q = __hmul2(__hadd2(*reinterpret_cast<const __nv_bfloat162*>(&n), less), sc);
+      v[j] = *reinterpret_cast<const uint32_t*>(&q);
+    }
+    out[4 * h] = __byte_perm(v[0], v[1], 0x5410), out[4 * h + 1] = __byte_perm(v[2], v[3], 0x5410);
+    out[4 * h + 2] = __byte_perm(v[0], v[1], 0x7632), out[4 * h + 3] = __byte_perm(v[2], v[3], 0x7632);
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    __stcs(reinterpret_cast<uint4*>(dst) + i, make_uint4(out[4 * i], out[4 * i + 1], out[4 * i + 2], out[4 * i + 3]));
+}
+
+template <int DH, typename T, int COLS>
+__global__ void __launch_bounds__(256) cache_read_kernel(const CacheRowsArgs a, unsigned cols) {
+  pdl_trigger();
+  pdl_wait();
+  using L = cache4::Layout<DH>;
+  const unsigned warp = (blockIdx.x * blockDim.x + threadIdx.x) >> 5;
+  const unsigned group = warp / cols, col = (warp - group * cols) * COLS;
+  const int blk = (threadIdx.x & 31) % (DH / cache4::kBlock);
+  const Spot s = find_spot<DH>(a, group);
+  if (!s.on) return;
+  uint2 w[COLS];
+  uint32_t sb[COLS];
+#pragma unroll
+  for (int c = 0; c < COLS; ++c) {
+    const bool value = col + c >= static_cast<unsigned>(a.c.Hkv);
+    const unsigned head = col + c - (value ? a.c.Hkv : 0);
+    const unsigned char* half = s.page + static_cast<size_t>(head) * L::BLOCK + (value ? L::V_OFF : 0);
+    w[c] = *reinterpret_cast<const uint2*>(half + s.in_page * L::CODE_ROW + blk * 8);
+    sb[c] = half[L::CODES + s.in_page * L::SCALE_ROW + blk];
+  }
+#pragma unroll
+  for (int c = 0; c < COLS; ++c) {
+    const bool value = col + c >= static_cast<unsigned>(a.c.Hkv);
+    const unsigned head = col + c - (value ? a.c.Hkv : 0);
+    decode16(static_cast<T*>(value ? a.v : a.k) + s.row * a.ld + head * DH + blk * cache4::kBlock, w[c], sb[c]);
+  }
+}
+
+template <int DH, typename T, int COLS>
+cudaError_t launch_cols(const CacheRowsArgs& a, bool write, long long groups, cudaStream_t st) {
+  const unsigned cols = 2u * a.c.Hkv / COLS;
+  const long long blocks = (groups * cols + 7) / 8;
+  if (blocks > 0x0fffffffLL) return cudaErrorInvalidValue;  // the warps' numbers are 32 bits
+  const cudaError_t e = launch_pdl(write ? cache_write_kernel<DH, T, COLS> : cache_read_kernel<DH, T, COLS>,
+                                   dim3(static_cast<unsigned>(blocks)), dim3(256), 0, st, a, cols);
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 template <int DH, typename T>
 cudaError_t launch_rows(const CacheRowsArgs& a, bool write, cudaStream_t st) {
   constexpr int TOK = 32 / (DH / cache4::kBlock);
-  const long long rows = static_cast<long long>(a.c.n_seqs) * a.M;
-  const long long warps = (rows + TOK - 1) / TOK * (2 * a.c.Hkv);
-  const long long blocks = (warps + 7) / 8;
-  if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
-  const dim3 grid(static_cast<unsigned>(blocks));
-  const cudaError_t e = launch_pdl(write ? cache_write_kernel<DH, T> : cache_read_kernel<DH, T>, grid, dim3(256), 0, st, a);
-  return e != cudaSuccess ? e : cudaGetLastError();
+  const long long groups = (static_cast<long long>(a.c.n_seqs) * a.M + TOK - 1) / TOK;
+  // four columns a warp once that leaves every SM its 64 warps
+  if (a.c.Hkv % 2 == 0 && groups * 2 * a.c.Hkv / 4 >= 148 * 64) return launch_cols<DH, T, 4>(a, write, groups, st);
+  return launch_cols<DH, T, 1>(a, write, groups, st);
 }
 
 cudaError_t launch_any(const CacheRowsArgs& a, int dh, bool bf16, bool write, cudaStream_t st) {

@@ -89,6 +89,14 @@ __device__ __forceinline__ uint32_t encode_value(float x, float s, float rs) {
   return static_cast<uint32_t>(static_cast<int>(q) + 8);
 }
 
+// encode_value for a bf16 x and a scale whose quotients stay below 7.5 in magnitude: q + 8 in the low byte.
+// x and s have 8 and 4 significant bits, so x / s is a tie or at least 2^-12 off one: rounding
+// x * rs, which is within 2^-22 of it, to steps of 2^-14 puts the ties back where they belong, and
+// the second sum rounds to the nearest integer. Its constant is 1.5 * 2^23 + 8 less the first's 1.5 * 2^9.
+__device__ __forceinline__ uint32_t encode_short(float x, float rs) {
+  return __float_as_uint(fmaf(x, rs, 768.f) + 12582152.f);
+}
+
 }  // namespace cache4
 
 struct CacheRowsArgs {
