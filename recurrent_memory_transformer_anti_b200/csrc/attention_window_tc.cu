@@ -14,22 +14,34 @@
 // 128, or 64, 32, 16 and 8 rows where the sinks end inside the tile: sinks cost their own rows,
 // not a tile of their own.
 //
-// One persistent CTA per SM, 12 warps:
+// One persistent CTA per SM, 20 warps:
 //   warp 0       one thread: TMA loads of the Q tiles and of the K and V rings;
-//   warp 1       TMEM allocation; one thread issues S = Q K^T and O += P V for A and B in turn
-//                (S of a tile's next keys before P V of its current ones, where P has columns of its
-//                own: head_dim 64; at 128 P overwrites S, and the next S follows P V in the pipe);
-//   warps 2-3    look through every V tile that some row sees only in part, before its P V: rows
+//   warps 1-     one thread each: TMEM allocation (warp 1), S = Q K^T and O += P V. At head_dim 64 each
+//                query tile has an issuing thread, S of its next keys before P V of its current ones
+//                (P has TMEM columns of its own); at 128, where P overwrites S and the next S follows
+//                P V in the pipe, one thread issues for both in turn (two threads mix their
+//                MMAs, which doubles each product's latency: 139 us for six prompts of up to 2063 rows,
+//                window 777, against 111);
+//   up to 3      look through every V tile that some row sees only in part, before its P V: rows
 //                behind the sequence's end, and rows that hold a value that is not finite, are
 //                zeroed (0 * inf would reach rows that do not see them); the latter are noted
 //                in a bit mask, and the rows that do see one give NaN;
-//   warps 4-7    softmax of A, one query row a thread; warps 8-11 the same for B.
-// The running maximum is only raised when it grows by more than 2^8 (weights stay <= 256, held as
-// bf16: an operand pair has one type). Every wait is bounded; a timeout drains in-flight copies
-// and MMAs, frees TMEM and sets the error word.
+//   warps 4-11   softmax of A, 12-19 of B: two threads a row, 64 columns each.
+// A row's reference (what its scores are taken relative to) is the maximum of the first tile it sees;
+// later tiles take their exponentials against it in one pass, and only a tile whose weights add
+// up to more than 2^12 is gone through again for its maximum, with O rescaled: no weight passes 2^12 (they
+// are held as bf16, whose relative precision is the same everywhere; an operand pair has one type).
+// Every wait is bounded; a timeout drains in-flight copies and MMAs, frees TMEM and sets the
+// error word.
 //
-// Bound: at head_dim 64 the 16,384 exponentials of a 128 x 128 tile (1024 cycles of the special
-// function unit, against 512 of MMA), at 128 MMA and exponentials alike.
+// Bound: the 32,768 exponentials of two 128 x 128 tiles take the special function unit 2048 cycles
+// (the MMAs 1024, or 2048 at head_dim 128); the step takes 4,500 at head_dim 64. With one
+// query tile in flight it takes 3,200, with the exponentials left out 3,700: what is left is the latency
+// of each softmax warp's own chain (barriers, TMEM accesses, one dependent instruction after
+// another), which four such warps per scheduler hide only in part, since they run in step. Measured and not better: one
+// thread a row with 168 or 200 registers (4,840), four query tiles against 64-key tiles (4,750), one issuing
+// thread that takes whatever is ready (4,800), longer waits between polls, a head start for A.
+// 65,536 tokens, 32/8 heads of 64, window 1024, 4 sinks: 1.20 ms, 455 TFLOP/s.
 #include <cuda.h>
 
 #include "cache4.cuh"
@@ -47,6 +59,8 @@ struct WtCfg {
   static constexpr int NSUB = HD / 64;
   static constexpr int TILE = NSUB * SUB;
   static constexpr bool OVERLAY = HD == 128;  // P in S's columns (512 TMEM columns hold no more)
+  static constexpr int NX = OVERLAY ? 2 : 1;       // query tiles of an issuing thread (warps 1 .. 2 / NX)
+  static constexpr int SEERS = 3 - 2 / NX;         // warps that look through V tiles (the rest up to warp 3)
   static constexpr int QST = HD == 64 ? 2 : 1, KST = HD == 64 ? 3 : 2;
   static constexpr int Q_OFF = 0;  // [x][QST]
   static constexpr int K_OFF = Q_OFF + 2 * QST * TILE;
@@ -56,9 +70,10 @@ struct WtCfg {
   static constexpr int QFULL = 0, QEMPTY = QFULL + 2 * QST, KFULL = QEMPTY + 2 * QST, KEMPTY = KFULL + KST,
                        VFULL = KEMPTY + KST, VEMPTY = VFULL + KST, VSEEN = VEMPTY + KST, SFULL = VSEEN + KST,
                        SFREE = SFULL + 2, PREADY = SFREE + 2, OREADY = PREADY + 2, OFREE = OREADY + 2,
-                       DRAIN = OFREE + 2, NBAR = DRAIN + 1;
+                       DRAIN = OFREE + 2, NBAR = DRAIN + 2;
   static constexpr int BAD_OFF = BAR_OFF + ((NBAR * 8 + 15) / 16) * 16;  // [KST][4] words: rows not finite
-  static constexpr int SLOT_OFF = BAD_OFF + KST * 16;
+  static constexpr int MX_OFF = BAD_OFF + KST * 16;   // [2 tiles][2 halves][128 rows] fp32: maxima, then sums
+  static constexpr int SLOT_OFF = MX_OFF + 2 * 2 * 128 * 4;
   static constexpr int SMEM = 1024 + SLOT_OFF + 16;
   static constexpr int S_COL = 0, O_COL = 256, P_COL = OVERLAY ? 0 : 256 + 2 * HD;
   static constexpr int P_STEP = OVERLAY ? 128 : 64;
@@ -75,6 +90,7 @@ struct WtArgs {
   int tq;      // tokens of a tile
   int window, sinks;
   int blocks, items;
+  int step_hc, step_g, step_b;  // what grid-size items on adds to an item's head chunk, sequence and block
 };
 
 struct WtMaps {
@@ -82,20 +98,42 @@ struct WtMaps {
   CUtensorMap kv[5];  // box 64 columns x 128 >> i rows
 };
 
+// Where in the items a CTA is: head chunk fastest, then sequence, then block of tokens (the last
+// first: long histories first). Moved on without a division.
+struct Place {
+  int it, hc, g, blk;
+  __device__ __forceinline__ explicit Place(const WtArgs& a) {
+    it = blockIdx.x;
+    const int per = a.Hkv * a.chunks, r = it / per;
+    hc = it - r * per;
+    blk = r / a.G;
+    g = r - blk * a.G;
+  }
+  __device__ __forceinline__ void next(const WtArgs& a) {
+    it += gridDim.x;
+    hc += a.step_hc;
+    g += a.step_g;
+    blk += a.step_b;
+    if (hc >= a.Hkv * a.chunks) hc -= a.Hkv * a.chunks, ++g;
+    if (g >= a.G) g -= a.G, ++blk;
+  }
+};
+
 // A work item: two tiles of tq tokens from token a0 on (see the file comment for lo, sp and u).
 struct Item {
   int g, kvh, h0, nh, a0, T, lo, sp, nt, last;
 };
 
-__device__ __forceinline__ Item item_of(const WtArgs& a, int it) {
+__device__ __forceinline__ Item item_of(const WtArgs& a, const Place& p) {
   Item m;
-  const int per = a.G * a.Hkv * a.chunks;
-  const int r = it % per;
-  m.a0 = (a.blocks - 1 - it / per) * 2 * a.tq;  // long histories first
-  const int hc = r % (a.Hkv * a.chunks);
-  m.g = r / (a.Hkv * a.chunks);
-  m.kvh = hc / a.chunks;
-  const int c = hc % a.chunks;
+  m.a0 = (a.blocks - 1 - p.blk) * 2 * a.tq;
+  m.g = p.g;
+  m.kvh = p.hc;
+  int c = 0;
+  if (a.chunks > 1) {
+    m.kvh = p.hc / a.chunks;
+    c = p.hc - m.kvh * a.chunks;
+  }
   m.h0 = m.kvh * a.group + c * a.heads;
   m.nh = min(a.heads, a.group - c * a.heads);
   m.T = a.lens ? min(__ldg(a.lens + m.g), a.M) : a.M;
@@ -110,11 +148,11 @@ __device__ __forceinline__ Item item_of(const WtArgs& a, int it) {
     else
       m.lo = 0;
   }
-  m.nt = (m.sp + m.last - m.lo + 128) / 128;
+  m.nt = (m.sp + m.last - m.lo + 128) >> 7;
   return m;
 }
 
-// Tile x (0: A, 1: B) of an item: its tokens, and the u they see at least and at most.
+// Query tile x (0: A, 1: B) of an item: its tokens, and the u they see at least and at most.
 struct Half {
   bool on;
   int b0, b1;         // first and last token
@@ -140,11 +178,11 @@ __device__ __forceinline__ bool partial(const WtArgs& a, const Item& m, int t) {
 
 // The tiles of this CTA's items in order, from before the first; tau numbers them (ring stages).
 struct Walk {
-  int it, t, tau;
+  int t, tau;
+  bool begun;
+  Place p;
   Item m;
-  __device__ __forceinline__ Walk() : it(static_cast<int>(blockIdx.x) - static_cast<int>(gridDim.x)), t(0), tau(-1) {
-    m.nt = 0;
-  }
+  __device__ __forceinline__ explicit Walk(const WtArgs& a) : t(0), tau(-1), begun(false), p(a) { m.nt = 0; }
   // to the next tile; false past the last
   __device__ __forceinline__ bool next(const WtArgs& a) {
     ++t;
@@ -152,20 +190,22 @@ struct Walk {
     if (t < m.nt) return true;
     t = 0;
     do {
-      it += gridDim.x;
-      if (it >= a.items) return false;
-      m = item_of(a, it);
+      if (begun) p.next(a);
+      begun = true;
+      if (p.it >= a.items) return false;
+      m = item_of(a, p);
     } while (m.nt == 0);
     return true;
   }
 };
-// Tiles that a half needs: f .. l, and those of the sinks.
+
+// Key tiles that a query tile needs: f .. l, and those of the sinks (l = -1: none).
 struct Need {
   int f, l;
 };
 __device__ __forceinline__ Need need_of(const WtArgs& a, const Item& m, int x) {
   const Half h = half_of(a, m, x);
-  return {h.lo0 / 128, h.on ? h.hi1 / 128 : -1};
+  return {h.lo0 >> 7, h.on ? h.hi1 >> 7 : -1};
 }
 __device__ __forceinline__ bool needs(const WtArgs& a, const Need& n, int t) {
   return t <= n.l && (t >= n.f || 128 * t < a.sinks);
@@ -201,10 +241,17 @@ __device__ __forceinline__ void sub_pair(uint32_t& a, uint32_t& b, float c) {
   add_pair(x, y, -c, -c);
   a = __float_as_uint(x), b = __float_as_uint(y);
 }
+// v, as a value the compiler knows nothing of: what is computed from it is computed where it is used, and
+// not kept in registers around a loop
+__device__ __forceinline__ int fresh(int v) {
+  int r;
+  asm volatile("mov.b32 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
 __device__ __forceinline__ float u2f(uint32_t u) { return __uint_as_float(u); }
 
 template <int HD>
-__global__ void __launch_bounds__(384, 1)
+__global__ void __launch_bounds__(640, 1)
     window_tc_kernel(const __grid_constant__ WtMaps maps, const __grid_constant__ WtArgs a) {
   using C = WtCfg<HD>;
   extern __shared__ uint8_t smem_raw[];
@@ -220,8 +267,9 @@ __global__ void __launch_bounds__(384, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::NBAR; ++i) {
       int n = 1;
-      if (i >= C::VSEEN && i < C::VSEEN + C::KST) n = 64;
-      if ((i >= C::SFREE && i < C::OREADY) || (i >= C::OFREE && i < C::DRAIN)) n = 128;
+      if (i >= C::VSEEN && i < C::VSEEN + C::KST) n = 32 * C::SEERS;
+      if ((i >= C::KEMPTY && i < C::VFULL) || (i >= C::VEMPTY && i < C::VSEEN)) n = 2;
+      if ((i >= C::SFREE && i < C::OREADY) || (i >= C::OFREE && i < C::DRAIN)) n = 256;
       sm100::mbar_init(bar(i), n);
     }
     *abort_flag = 0;
@@ -242,7 +290,7 @@ __global__ void __launch_bounds__(384, 1)
     if (lane == 0) {
       bool ok = true;
       int nq[2] = {0, 0}, nk = 0, nv = 0;  // loads issued: Q tiles of A and B, K tiles, V tiles
-      Walk w;
+      Walk w(a);
       // rows u0 .. u0 + 127 of the item's keys (column col of the packed rows) into a ring tile
       auto load_tile = [&](uint32_t dst, uint32_t full, int col) {
         sm100::mbar_arrive_expect_tx(full, C::TILE);
@@ -301,104 +349,127 @@ __global__ void __launch_bounds__(384, 1)
           sm100::mbar_wait_drain(bar(C::VFULL + n % C::KST), (n / C::KST) & 1);
       }
     }
-  } else if (warp == 1) {
+  } else if (warp <= 2 / C::NX) {
     if (lane == 0) {
+      const int x0 = C::NX == 1 ? warp - 1 : 0;
       constexpr uint32_t idS = sm100::idesc_f32acc(128, 128, OpFormat<bf16>::value);
       constexpr uint32_t idO = sm100::idesc_f32acc_bmn(128, HD, OpFormat<bf16>::value);
+      const uint64_t dq = sm100::smem_desc_k128(base + C::Q_OFF), dk = sm100::smem_desc_k128(base + C::K_OFF),
+                     dv = sm100::smem_desc_mn128(base + C::V_OFF, C::SUB);
       bool ok = true;
-      int nq[2] = {-1, -1};                          // the Q tile in use, counted
-      int ns[2] = {0, 0}, np[2] = {0, 0}, no[2] = {0, 0};  // S issued, P V issued, items begun
-      bool fresh_q[2] = {true, true}, fresh_o[2] = {true, true};  // the next S / P V is an item's first
+      // per query tile: Q tile in use, S and P V issued, items begun; the next S / P V is an item's
+      // first; the current key tile is needed
+      int nq[C::NX], ns[C::NX], np[C::NX], no[C::NX];
+      bool fresh_q[C::NX], fresh_o[C::NX], p[C::NX];
+      Need nn[C::NX];
+#pragma unroll
+      for (int i = 0; i < C::NX; ++i) {
+        nq[i] = -1, ns[i] = np[i] = no[i] = 0;
+        fresh_q[i] = fresh_o[i] = true;
+        p[i] = false;
+        nn[i] = {0, -1};
+      }
+      int st = 0, pst = 0;  // ring stages of the next key tile and of the current one
+      uint32_t ph = 0, pph = 0;
       auto wait = [&](int b, uint32_t parity) { return sm100::mbar_wait(bar(b), parity & 1u, abort_flag); };
-      auto issue_s = [&](int x, int tau, bool last) -> bool {
-        const int st = tau % C::KST;
-        if (fresh_q[x]) ++nq[x];
-        const int id = x * C::QST + nq[x] % C::QST;
-        if (fresh_q[x] && !wait(C::QFULL + id, nq[x] / C::QST)) return false;
-        fresh_q[x] = false;
-        if (!wait(C::KFULL + st, tau / C::KST)) return false;
-        if (!C::OVERLAY && ns[x] > 0 && !wait(C::SFREE + x, ns[x] - 1)) return false;
-        sm100::tc_fence_after();
-#pragma unroll
-        for (int k = 0; k < HD / 16; ++k) {
-          const int sb = k >> 2, kk = k & 3;
-          const uint64_t ad = sm100::smem_desc_k128(base + C::Q_OFF + id * C::TILE + sb * C::SUB) + 2ull * kk;
-          const uint64_t bd = sm100::smem_desc_k128(base + C::K_OFF + st * C::TILE + sb * C::SUB) + 2ull * kk;
-          sm100::mma_bf16(tmem + C::S_COL + 128 * x, ad, bd, idS, k > 0);
-        }
-        sm100::mma_commit(bar(C::SFULL + x));
-        if (last) sm100::mma_commit(bar(C::QEMPTY + id));  // the item's last S of x has read its Q
-        ++ns[x];
-        return true;
-      };
-      auto issue_pv = [&](int x, int tau) -> bool {
-        const int st = tau % C::KST;
-        if (!wait(C::PREADY + x, np[x]) || !wait(C::VSEEN + st, tau / C::KST)) return false;
-        // the first P V of an item overwrites O: the previous item's must have been read
-        if (fresh_o[x] && no[x] > 0 && !wait(C::OFREE + x, no[x] - 1)) return false;
-        sm100::tc_fence_after();
-#pragma unroll
-        for (int k = 0; k < 128 / 16; ++k) {  // P from TMEM: 16 keys per step = 8 columns of pairs
-          const uint64_t bd = sm100::smem_desc_mn128(base + C::V_OFF + st * C::TILE + k * 2048, C::SUB);
-          sm100::mma_f16_tmem_a(tmem + C::O_COL + HD * x, tmem + C::P_COL + C::P_STEP * x + 8 * k, bd, idO,
-                                !fresh_o[x] || k > 0);
-        }
-        sm100::mma_commit(bar(C::OREADY + x));
-        if (fresh_o[x]) ++no[x];
-        fresh_o[x] = false;
-        ++np[x];
-        return true;
-      };
-      // S of the next tile and P V of the current one, for A and B in turn
-      Walk nxt;
-      int ct = 0, ctau = -1;
-      Need cn[2] = {{0, -1}, {0, -1}}, nn[2] = {{0, -1}, {0, -1}};
+      // S of the next key tile and P V of the current one, in turn
+      Walk nxt(a);
+      bool cur = false, cur_first = false;  // there is a current key tile; it is an item's first
       while (ok) {
         const bool more = nxt.next(a);
-        if (more && nxt.t == 0) {
-          for (int x = 0; x < 2; ++x) {
-            nn[x] = need_of(a, nxt.m, x);
-            fresh_q[x] = true;
+#pragma unroll
+        for (int turn = 0; turn < 2 * C::NX; ++turn) {
+          if (!ok) break;
+          const int i = turn / 2, x = x0 + i;
+          if (((turn & 1) == 0) != C::OVERLAY) {
+            if (more && nxt.t == 0) {
+              nn[i] = need_of(a, nxt.m, x);
+              fresh_q[i] = true;
+            }
+            const bool s = more && needs(a, nn[i], nxt.t);
+            if (s) {
+              if (fresh_q[i]) ++nq[i];
+              const int qs = nq[i] % C::QST;
+              ok = (!fresh_q[i] || wait(C::QFULL + x * C::QST + qs, nq[i] / C::QST)) && wait(C::KFULL + st, ph) &&
+                   (C::OVERLAY || ns[i] == 0 || wait(C::SFREE + x, ns[i] - 1));
+              if (!ok) break;
+              fresh_q[i] = false;
+              ++ns[i];
+              sm100::tc_fence_after();
+              const uint64_t ad = dq + static_cast<uint32_t>((x * C::QST + qs) * (C::TILE >> 4));
+              const uint64_t bd = dk + static_cast<uint32_t>(st * (C::TILE >> 4));
+#pragma unroll
+              for (int k = 0; k < HD / 16; ++k) {
+                const uint32_t at = ((k >> 2) * C::SUB + (k & 3) * 32) >> 4;
+                sm100::mma_bf16(tmem + C::S_COL + 128 * x, ad + at, bd + at, idS, k > 0);
+              }
+              sm100::mma_commit(bar(C::SFULL + x));
+              sm100::mma_commit(bar(C::KEMPTY + st));
+              if (nxt.t == nn[i].l) sm100::mma_commit(bar(C::QEMPTY + x * C::QST + qs));  // the item's last S
+            } else if (more) {  // not before it has landed: two arrivals in one phase would pass for both tiles'
+              ok = wait(C::KFULL + st, ph);
+              if (!ok) break;
+              sm100::mbar_arrive(bar(C::KEMPTY + st));
+            }
+            if (C::OVERLAY) p[i] = s;
+          } else if (cur) {
+            if (cur_first) fresh_o[i] = true;
+            if (p[i]) {
+              // the first P V of an item overwrites O: the previous item's must have been read
+              ok = wait(C::PREADY + x, np[i]) && wait(C::VSEEN + pst, pph) &&
+                   (!fresh_o[i] || no[i] == 0 || wait(C::OFREE + x, no[i] - 1));
+              if (!ok) break;
+              ++np[i];
+              sm100::tc_fence_after();
+              const uint64_t bd = dv + static_cast<uint32_t>(pst * (C::TILE >> 4));
+#pragma unroll
+              for (int k = 0; k < 128 / 16; ++k)  // P from TMEM: 16 keys per step = 8 columns of pairs
+                sm100::mma_f16_tmem_a(tmem + C::O_COL + HD * x, tmem + C::P_COL + C::P_STEP * x + 8 * k,
+                                      bd + static_cast<uint32_t>(k * 2048 >> 4), idO, !fresh_o[i] || k > 0);
+              sm100::mma_commit(bar(C::OREADY + x));
+              sm100::mma_commit(bar(C::VEMPTY + pst));
+              if (fresh_o[i]) ++no[i];
+              fresh_o[i] = false;
+            } else {
+              ok = wait(C::VSEEN + pst, pph);
+              if (!ok) break;
+              sm100::mbar_arrive(bar(C::VEMPTY + pst));
+            }
           }
         }
+        if (!ok || !more) break;
+        if (!C::OVERLAY)
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          if (!ok) break;
-          const bool s = more && needs(a, nn[x], nxt.t), p = ctau >= 0 && needs(a, cn[x], ct);
-          if (ct == 0) fresh_o[x] = true;
-          if (C::OVERLAY && p) ok = issue_pv(x, ctau);
-          if (ok && s) ok = issue_s(x, nxt.tau, nxt.t == nn[x].l);
-          if (ok && more && x == 1) sm100::mma_commit(bar(C::KEMPTY + nxt.tau % C::KST));
-          if (!C::OVERLAY && ok && p) ok = issue_pv(x, ctau);
+          for (int i = 0; i < C::NX; ++i) p[i] = needs(a, nn[i], nxt.t);
+        cur = true;
+        cur_first = nxt.t == 0;
+        pst = st;
+        pph = ph;
+        if (++st == C::KST) {
+          st = 0;
+          ph ^= 1u;
         }
-        if (ok && ctau >= 0) sm100::mma_commit(bar(C::VEMPTY + ctau % C::KST));
-        if (!more) break;
-        ct = nxt.t;
-        ctau = nxt.tau;
-        cn[0] = nn[0];
-        cn[1] = nn[1];
       }
       if (!ok) {
         if (a.err) atomicOr(a.err, kErrTimeoutMma);
-        sm100::mma_commit(bar(C::DRAIN));
-        sm100::mbar_wait_drain(bar(C::DRAIN), 0);
+        sm100::mma_commit(bar(C::DRAIN + x0));
+        sm100::mbar_wait_drain(bar(C::DRAIN + x0), 0);
       }
     }
     __syncwarp();
   } else if (warp < 4) {
-    const int c = threadIdx.x - 64;
     bool ok = true;
-    Walk w;
+    Walk w(a);
     while (w.next(a)) {
       const int st = w.tau % C::KST;
       ok = __all_sync(0xffffffffu, sm100::mbar_wait(bar(C::VFULL + st), (w.tau / C::KST) & 1, abort_flag));
       if (!ok) break;
       if (partial(a, w.m, w.t)) {
-        // two rows a thread; 16 bytes at a time, each lane from another column of the row's
+        // some rows a thread; 16 bytes at a time, each lane from another column of the row's
         // 128 bytes (the order within a row does not matter here)
 #pragma unroll 1
-        for (int rr = 0; rr < 2; ++rr) {
-          const int row = c + 64 * rr, u = 128 * w.t + row;
+        for (int rr = 0; rr < 4 / C::SEERS; ++rr) {
+          const int row = 32 * (C::SEERS * rr + 3 - warp) + lane, u = 128 * w.t + row;
           const bool behind = u >= w.m.sp && w.m.lo + u - w.m.sp >= w.m.T;
           uint4* const p = reinterpret_cast<uint4*>(smem + C::V_OFF + st * C::TILE + row * 128);
           __nv_bfloat162 acc = __float2bfloat162_rn(0.f);
@@ -426,173 +497,231 @@ __global__ void __launch_bounds__(384, 1)
     }
     if (!ok && lane == 0 && a.err) atomicOr(a.err, kErrTimeoutEpilogue);
   } else {
-    const int x = (warp - 4) >> 2, quarter = warp & 3;
+    // Two threads a row, 64 columns of S each: four softmax warps per scheduler, so that one's
+    // barriers, loads and maxima run under another's exponentials.
+    const int x = (warp - 4) >> 3, half = ((warp - 4) >> 2) & 1, quarter = warp & 3;
     const int r = quarter * 32 + lane;  // row of the tile = TMEM lane
     const uint32_t loff = static_cast<uint32_t>(quarter * 32) << 16;
-    const uint32_t tS = tmem + loff + C::S_COL + 128 * x, tO = tmem + loff + C::O_COL + HD * x,
-                   tP = tmem + loff + C::P_COL + C::P_STEP * x;
+    const uint32_t tS = tmem + loff + C::S_COL + 128 * x + 64 * half;
+    const uint32_t tO = tmem + loff + C::O_COL + HD * x + HD / 2 * half;
+    const uint32_t tP = tmem + loff + C::P_COL + C::P_STEP * x + 32 * half;
+    float* const mx_own = reinterpret_cast<float*>(smem + C::MX_OFF) + (2 * x + half) * 128 + r;
+    const float* const mx_other = reinterpret_cast<float*>(smem + C::MX_OFF) + (2 * x + 1 - half) * 128 + r;
+    const int pair = 1 + 4 * x + quarter;  // named barrier of the two warps of these rows
+    auto meet = [&]() { asm volatile("bar.sync %0, 64;" ::"r"(pair) : "memory"); };
+    auto meet_any = [&](bool v) {  // and: does any of their threads say so
+      uint32_t any;
+      asm volatile(
+          "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+          "bar.red.or.pred q, %2, 64, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+          : "=r"(any)
+          : "r"(static_cast<uint32_t>(v)), "r"(pair)
+          : "memory");
+      return any != 0;
+    };
+    // A wait that gave up (or saw the abort flag) does not leave the loop: the other half's warp would
+    // wait for this one for good. The rest is then gone through without waiting, its results not used.
+    bool dead = false;
+    auto await = [&](int b, int phase) {
+      if (!__all_sync(0xffffffffu, sm100::mbar_wait(bar(b), phase & 1u, abort_flag))) dead = true;
+    };
     const float sl2 = rsqrtf(static_cast<float>(HD)) * 1.4426950408889634f;  // 1/sqrt(dh) * log2(e)
-    const float raise = 8.f / sl2;  // the running maximum (of the raw scores) is only raised by that much
     const int hh = r / a.tq, tok = r - hh * a.tq;
-    bool ok = true;
     int n = 0;    // tiles of x processed so far (barrier phases)
     int tau = 0;  // tiles of the CTA passed
-    for (int it = blockIdx.x; it < a.items && ok; it += gridDim.x) {
-      const Item m = item_of(a, it);
-      const Half h = half_of(a, m, x);
-      const Need need = need_of(a, m, x);
+    for (Place place(a); place.it < a.items; place.next(a)) {
+      int nt, token, uhi, ulo, us, late_from, early_to, part_to, part_from;
+      Need need;
+      bool idle;
+      {
+        const Item m = item_of(a, place);
+        const Half h = half_of(a, m, x);
+        need = need_of(a, m, x);
+        nt = m.nt;
+        const int d = m.sp - m.lo;
+        token = h.b0 + tok;
+        uhi = token + d, ulo = max(token - a.window + 1, m.lo) + d, us = min(a.sinks, uhi + 1);
+        // the tiles in which some row of x sees only part (late: keys after it; early: keys that
+        // left its window), and those in which some row of the item does: before part_to, from part_from
+        late_from = h.hi0 - 126 <= 0 ? 0 : (h.hi0 - 126 + 127) >> 7;
+        early_to = (h.lo1 + 127) >> 7;
+        part_to = max((m.sp + 127) >> 7, m.last - a.window + 1 + d <= 0 ? 0 : (m.last - a.window + 1 + d + 127) >> 7);
+        part_from = m.a0 + d - 126 <= 0 ? 0 : (m.a0 + d - 126 + 127) >> 7;
+        idle = quarter * 32 >= m.nh * a.tq;  // warp-uniform: no row of this warp is used
+      }
       const int tau0 = tau;
-      tau += m.nt;
-      if (m.nt == 0 || !h.on) continue;
-      const bool idle = quarter * 32 >= m.nh * a.tq;  // warp-uniform: no row of this warp is used
-      const int token = h.b0 + tok, d = m.sp - m.lo;
-      const int uhi = token + d, ulo = max(token - a.window + 1, m.lo) + d, us = min(a.sinks, uhi + 1);
-      float m_use = -3e38f, l = 0.f;
+      tau += nt;
+      if (need.l < 0 || nt == 0) continue;
+      float m_use = -3e38f, l = 0.f;  // a row that has seen nothing keeps that: its weights are 2^-inf = 0
       bool poison = false, first = true;
-      for (int t = 0; t < m.nt; ++t) {
+      for (int t = 0; t <= need.l; ++t) {
         if (!needs(a, need, t)) continue;
-        ok = __all_sync(0xffffffffu, sm100::mbar_wait(bar(C::SFULL + x), n & 1, abort_flag));
-        if (!ok) break;
+        await(C::SFULL + x, n);
         if (idle) {  // the same waits and arrivals as the busy warps, in the same order
-          sm100::mbar_arrive(bar(C::SFREE + x));
-          if (n > 0) {
-            ok = __all_sync(0xffffffffu, sm100::mbar_wait(bar(C::OREADY + x), (n - 1) & 1, abort_flag));
-            if (!ok) break;
-          }
+          if (!C::OVERLAY) sm100::mbar_arrive(bar(C::SFREE + x));
+          if (n > 0) await(C::OREADY + x, n - 1);
           sm100::mbar_arrive(bar(C::PREADY + x));
           first = false;
           ++n;
           continue;
         }
         sm100::tc_fence_after();
-        uint32_t s[4][32];
-#pragma unroll
-        for (int q4 = 0; q4 < 4; ++q4) sm100::tmem_ld32(tS + 32 * q4, s[q4]);
-        sm100::tmem_wait_ld();
-        sm100::tc_fence_before();
-        if (!C::OVERLAY) sm100::mbar_arrive(bar(C::SFREE + x));
-        const int u0 = 128 * t;
-        if (u0 + 127 > h.hi0) {  // keys after some row's own
-          const int vis = uhi - u0;
-#pragma unroll
-          for (int q4 = 0; q4 < 4; ++q4)
+        const bool late = t >= late_from, early = t < early_to;
+        const int u0 = 128 * t + 64 * half;
+        // 32 columns from q on, masked keys at -inf
+        auto mask = [&](uint32_t (&s)[32], int q) {
+          const int vis = fresh(uhi - u0) - q;
+          if (late && __any_sync(0xffffffffu, vis < 31)) {
 #pragma unroll
             for (int i = 0; i < 32; ++i)
-              if (32 * q4 + i > vis) s[q4][i] = __float_as_uint(-INFINITY);
-        }
-        if (u0 < h.lo1) {  // keys that left some row's window: from the sinks' end to its oldest
-          const int from = max(us - u0, 0);
-          const unsigned gone = static_cast<unsigned>(max(ulo - u0 - from, 0));
-#pragma unroll
-          for (int q4 = 0; q4 < 4; ++q4)
+              if (i > vis) s[i] = __float_as_uint(-INFINITY);
+          }
+          const int from = max(fresh(us - u0) - q, 0);
+          const int gone = fresh(ulo - u0) - q - from;
+          if (early && __any_sync(0xffffffffu, gone > 0 && from < 32)) {
 #pragma unroll
             for (int i = 0; i < 32; ++i)
-              if (static_cast<unsigned>(32 * q4 + i - from) < gone) s[q4][i] = __float_as_uint(-INFINITY);
-        }
-        if (partial(a, m, t)) {
-          const int st = (tau0 + t) % C::KST;
-          ok = __all_sync(0xffffffffu,
-                          sm100::mbar_wait(bar(C::VSEEN + st), ((tau0 + t) / C::KST) & 1, abort_flag));
-          if (!ok) break;
-          const uint32_t b0 = bad[4 * st], b1 = bad[4 * st + 1], b2 = bad[4 * st + 2], b3 = bad[4 * st + 3];
-          if (b0 | b1 | b2 | b3) {  // rare
-            for (int e = 0; e < 128; ++e) {
-              const uint32_t wd = e < 64 ? (e < 32 ? b0 : b1) : (e < 96 ? b2 : b3);
-              const int u = u0 + e;
-              if (((wd >> (e & 31)) & 1u) && ((u >= ulo && u <= uhi) || u < us)) poison = true;
+              if (static_cast<unsigned>(i - from) < static_cast<unsigned>(max(gone, 0))) s[i] = __float_as_uint(-INFINITY);
+          }
+        };
+        float corr = 1.f, sum;
+        bool rescale = false, over = first, redone = first;
+        uint32_t pk[32];
+        for (int tries = first ? 1 : 0;; ++tries) {
+          if (tries > 0) {
+            redone = true;
+            // the row maximum, over both halves
+            float mxp[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+            for (int q = 0; q < 64; q += 32) {
+              uint32_t s[32];
+              sm100::tmem_ld32(tS + q, s);
+              sm100::tmem_wait_ld();
+              mask(s, q);
+#pragma unroll
+              for (int i = 0; i < 32; i += 2)
+                mxp[(i >> 1) & 3] = max3(mxp[(i >> 1) & 3], u2f(s[i]), u2f(s[i + 1]));
+            }
+            float mx = fmaxf(fmaxf(mxp[0], mxp[1]), fmaxf(mxp[2], mxp[3]));
+            // rows whose weights stayed small say so by NaN: they keep their reference
+            *mx_own = over ? mx : NAN;
+            meet();
+            const float other = *mx_other;
+            meet();
+            const bool raise = over || other == other;
+            if (raise) {
+              // a half that was not over says nothing of its maximum, which is then not above the reference
+              // by more than its sum allows
+              mx = fmaxf(over ? mx : m_use, other == other ? other : m_use);
+              if (mx > m_use) {
+                corr = ex2((m_use - mx) * sl2);
+                m_use = mx;
+                rescale = !first;
+              }
             }
           }
+          // s * sl2 - m * sl2 in one rounding is off by up to 2^-24 of m * sl2: where scores are that
+          // large the difference is taken first
+          const bool far = fabsf(m_use) > 4194304.f;
+          const bool any_far = __any_sync(0xffffffffu, far);
+          const float by = far ? m_use : 0.f, less = far ? 0.f : m_use * sl2;
+          float sp[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int q = 0; q < 64; q += 32) {
+            uint32_t c[32];
+            sm100::tmem_ld32(tS + q, c);
+            sm100::tmem_wait_ld();
+            if (late || early) mask(c, q);
+            if (any_far) {
+#pragma unroll
+              for (int i = 0; i < 32; i += 2) sub_pair(c[i], c[i + 1], by);
+            }
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+              fma_pair(c[i], c[i + 1], sl2, -less);
+              const float p0 = ex2(u2f(c[i])), p1 = ex2(u2f(c[i + 1]));
+              add_pair(sp[i & 2], sp[(i & 2) + 1], p0, p1);
+              pk[(q + i) >> 1] = pack2<bf16>(p0, p1);
+            }
+          }
+          sum = (sp[0] + sp[1]) + (sp[2] + sp[3]);
+          over = !(sum <= 4096.f);  // NaN too: gone through once more, to no effect
+          if (tries > 0 || !meet_any(over)) break;
         }
-        // row maximum over 4 independent partials (short dependency chains)
-        float mxp[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-        for (int q4 = 0; q4 < 4; ++q4)
-#pragma unroll
-          for (int i = 0; i < 32; i += 2)
-            mxp[(i >> 1) & 3] = max3(mxp[(i >> 1) & 3], u2f(s[q4][i]), u2f(s[q4][i + 1]));
-        const float mx = fmaxf(fmaxf(mxp[0], mxp[1]), fmaxf(mxp[2], mxp[3]));
-        float corr = 1.f;
-        bool rescale = false;
-        if (mx > m_use + raise) {  // a row that has seen nothing keeps -3e38: its weights are 2^-inf = 0
-          corr = ex2((m_use - mx) * sl2);
-          m_use = mx;
-          rescale = !first;
-        }
-        // s * sl2 - m * sl2 in one rounding is off by up to 2^-24 of m * sl2: where scores are that
-        // large the difference is taken first
-        float less = m_use * sl2;
-        const bool far = fabsf(m_use) > 4194304.f;
-        if (__any_sync(0xffffffffu, far)) {
-          const float by = far ? m_use : 0.f;  // the warp's other rows stay as they are
-#pragma unroll
-          for (int q4 = 0; q4 < 4; ++q4)
-#pragma unroll
-            for (int i = 0; i < 32; i += 2) sub_pair(s[q4][i], s[q4][i + 1], by);
-          if (far) less = 0.f;
-        }
+        sm100::tc_fence_before();
+        if (!C::OVERLAY) sm100::mbar_arrive(bar(C::SFREE + x));
+        if (C::OVERLAY && redone) meet();  // P goes where the other half's S was (else they met above)
         if (n > 0) {
           // P V of the tile before must be done before P and O change
-          ok = __all_sync(0xffffffffu, sm100::mbar_wait(bar(C::OREADY + x), (n - 1) & 1, abort_flag));
-          if (!ok) break;
+          await(C::OREADY + x, n - 1);
           sm100::tc_fence_after();
           if (__any_sync(0xffffffffu, rescale)) {
-            const float by = rescale ? corr : 1.f;
+            const float f = rescale ? corr : 1.f;
 #pragma unroll 1
-            for (int oc = 0; oc < HD / 16; ++oc) {
+            for (int oc = 0; oc < HD / 32; ++oc) {
               uint32_t o[16];
               sm100::tmem_ld16(tO + 16 * oc, o);
               sm100::tmem_wait_ld();
 #pragma unroll
-              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(u2f(o[i]) * by);
+              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(u2f(o[i]) * f);
               sm100::tmem_st16(tO + 16 * oc, o);
             }
           }
         }
-        // weights, packed in place (keys 2c, 2c + 1 in column c) and sent 32 keys at a time
-        float sp[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int q4 = 0; q4 < 4; ++q4) {
-#pragma unroll
-          for (int i = 0; i < 32; i += 2) {
-            fma_pair(s[q4][i], s[q4][i + 1], sl2, -less);
-            const float p0 = ex2(u2f(s[q4][i])), p1 = ex2(u2f(s[q4][i + 1]));
-            add_pair(sp[i & 2], sp[(i & 2) + 1], p0, p1);
-            s[q4][i >> 1] = pack2<bf16>(p0, p1);
+        sm100::tmem_st16(tP, pk);  // keys 2c, 2c + 1 in column c
+        sm100::tmem_st16(tP + 16, pk + 16);
+        l = l * corr + sum;
+        if (t < part_to || t >= part_from) {
+          const int st = (tau0 + t) % C::KST;
+          await(C::VSEEN + st, (tau0 + t) / C::KST);
+          const uint32_t b0 = bad[4 * st], b1 = bad[4 * st + 1], b2 = bad[4 * st + 2], b3 = bad[4 * st + 3];
+          if (b0 | b1 | b2 | b3) {  // rare
+            for (int e = 0; e < 128; ++e) {
+              const uint32_t wd = e < 64 ? (e < 32 ? b0 : b1) : (e < 96 ? b2 : b3);
+              const int u = 128 * t + e;
+              if (((wd >> (e & 31)) & 1u) && ((u >= ulo && u <= uhi) || u < us)) poison = true;
+            }
           }
-          sm100::tmem_st16(tP + 16 * q4, s[q4]);
         }
-        l = l * corr + ((sp[0] + sp[1]) + (sp[2] + sp[3]));
         sm100::tmem_wait_st();
         sm100::tc_fence_before();
         sm100::mbar_arrive(bar(C::PREADY + x));
         first = false;
         ++n;
       }
-      if (!ok) break;
-      // end of the item: O after its last P V, normalised and stored; then O is free again
-      ok = __all_sync(0xffffffffu, sm100::mbar_wait(bar(C::OREADY + x), (n - 1) & 1, abort_flag));
-      if (!ok) break;
+      // end of the item: the row's sum over both halves, and O after its last P V, normalised and
+      // stored; then O is free again
+      if (!idle) {
+        *mx_own = l;
+        meet();
+        l += *mx_other;  // the next item's first tile meets before it writes there again
+        meet();
+      }
+      await(C::OREADY + x, n - 1);
       sm100::tc_fence_after();
       const float inv = poison ? NAN : 1.f / l;
-      const bool row_out = hh < m.nh && token < m.T;
-      bf16* const dst = static_cast<bf16*>(a.out) +
-                        ((static_cast<size_t>(m.g) * a.M + token) * a.H + m.h0 + hh) * HD;
+      {
+        const Item m = item_of(a, place);  // again, rather than in registers through the tiles
+        const bool row_out = hh < m.nh && token < m.T;
+        bf16* const dst = static_cast<bf16*>(a.out) +
+                          ((static_cast<size_t>(m.g) * a.M + token) * a.H + m.h0 + hh) * HD + HD / 2 * half;
 #pragma unroll 1
-      for (int oc = 0; oc < (idle ? 0 : HD / 32); ++oc) {
-        uint32_t o[32];
-        sm100::tmem_ld32(tO + 32 * oc, o);
-        sm100::tmem_wait_ld();
-        if (row_out) {
-          float v[32];
+        for (int oc = 0; oc < (idle ? 0 : HD / 64); ++oc) {
+          uint32_t o[32];
+          sm100::tmem_ld32(tO + 32 * oc, o);
+          sm100::tmem_wait_ld();
+          if (row_out) {
+            float v[32];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = u2f(o[i]) * inv;
-          store32_16(dst + 32 * oc, v);
+            for (int i = 0; i < 32; ++i) v[i] = u2f(o[i]) * inv;
+            store32_16(dst + 32 * oc, v);
+          }
         }
       }
       sm100::tc_fence_before();
       sm100::mbar_arrive_relaxed(bar(C::OFREE + x));
     }
-    if (!ok && lane == 0 && a.err) atomicOr(a.err, kErrTimeoutEpilogue);
+    if (dead && lane == 0 && a.err) atomicOr(a.err, kErrTimeoutEpilogue);
   }
 
   sm100::tc_fence_before();
@@ -630,7 +759,11 @@ cudaError_t launch_hd(const WindowAttnArgs& w, cudaStream_t st) {
   cudaError_t e = allow_smem(reinterpret_cast<const void*>(window_tc_kernel<HD>), C::SMEM, done);
   if (e != cudaSuccess) return e;
   const int grid = a.items < 148 ? a.items : 148;  // one CTA per SM
-  e = launch_pdl(window_tc_kernel<HD>, dim3(grid), dim3(384), C::SMEM, st, maps, a);
+  const int per = a.Hkv * a.chunks, over = grid / per;
+  a.step_hc = grid - over * per;
+  a.step_b = over / a.G;
+  a.step_g = over - a.step_b * a.G;
+  e = launch_pdl(window_tc_kernel<HD>, dim3(grid), dim3(640), C::SMEM, st, maps, a);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
