@@ -297,7 +297,7 @@ __global__ void __launch_bounds__(32 * Shape<DH, NT>::WARPS, 1) cache_attn_kerne
       x.begin = 0;
       x.s = span_of<U::TOK>(a.span, x.len);
     } else {
-      int lo = 0, hi = kThreads - 1;  // the last run of sequences that begins at or before u
+      int lo = 0, hi = (n - 1) / run;  // the last run of sequences that begins at or before u
       while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
         if (pre[mid] <= u)
@@ -890,18 +890,15 @@ cudaError_t launch_decode(const CacheAttnArgs& c, cudaStream_t st) {
   }
   e = launch_pdl(kernel, dim3(p.ctas), dim3(32 * kWarps), smem, st, a);
   if (e == cudaSuccess && !p.whole) {
-    // many items: their rows together in 256 threads, one to four parts at a time; few: a row per
-    // CTA, with as many threads as it may have
-    const bool many = p.items >= 64;
-    int per = 8 * NT < a.rows ? 8 * NT : a.rows;
-    if (!many)
-      per = 1;
-    else if (per * (DH / 4) > 256)
-      per = 256 / (DH / 4);
-    const int most_rows = 8 * NT < a.rows ? 8 * NT : a.rows;
-    e = launch_pdl(cache_attn_join_kernel<DH, T, NT>,
-                   dim3(static_cast<unsigned>(p.items), (most_rows + per - 1) / per), dim3(many ? 256 : 1024), 0, st, a,
-                   p.warps, per);
+    // threads for a group of about four parts each of an item's parts (were they alike): its rows
+    // together, or fewer rows a CTA where that takes more than 1024
+    const int rows = 8 * NT < a.rows ? 8 * NT : a.rows;
+    const int want = static_cast<int>((p.warps + 4 * p.items - 1) / (4 * p.items));
+    int per = rows;
+    while (per > 1 && per * (DH / 4) * want > 1024) per = (per + 1) / 2;
+    const int threads = per * (DH / 4) * want < 1024 ? (per * (DH / 4) * want + 31) / 32 * 32 : 1024;
+    e = launch_pdl(cache_attn_join_kernel<DH, T, NT>, dim3(static_cast<unsigned>(p.items), (rows + per - 1) / per),
+                   dim3(threads), 0, st, a, p.warps, per);
   }
   return e != cudaSuccess ? e : cudaGetLastError();
 }

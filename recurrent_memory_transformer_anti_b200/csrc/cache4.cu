@@ -1,8 +1,9 @@
 // Writing rows into the 4-bit key/value cache, and reading them back (layout and arithmetic:
-// cache4.cuh). Both stream: one thread holds the 16 channels of one scale, so a block's maximum
-// needs no other lane, and a warp covers 512 channels of one head's keys or values -- 16, 8 or 4
-// tokens -- so that its codes and its scales each land in whole 32-byte sectors. A warp takes four
-// such (keys or values, head) columns of its tokens where there are warps enough, with their loads in
+// cache4.cuh). Both stream. Writing, a thread holds the 16 channels of one scale, so a block's maximum
+// needs no other lane and a scale is worked out once (8 channels a thread and an exchange: 26 us instead
+// of 22 for 67 MB of bf16); reading, it holds 8 channels, 16 bytes of bf16, so that each
+// store of a warp fills whole sectors (16 channels a thread: 22 us instead of 15). A warp takes
+// four (keys or values, head) columns of its tokens where there are warps enough, with their loads in
 // flight together and the tokens' pages looked up once.
 //
 // Bound by HBM if the arithmetic stays at about 5 instructions a channel: a bf16 channel is
@@ -24,11 +25,12 @@ struct Spot {
   int in_page;
 };
 
-template <int DH>
+// CH: channels of a thread
+template <int DH, int CH>
 __device__ __forceinline__ Spot find_spot(const CacheRowsArgs& a, unsigned group) {
-  constexpr unsigned BLK = DH / cache4::kBlock, TOK = 32 / BLK;
+  constexpr unsigned LANES = DH / CH, TOK = 32 / LANES;
   Spot s{};
-  const unsigned row = group * TOK + (threadIdx.x & 31u) / BLK;
+  const unsigned row = group * TOK + (threadIdx.x & 31u) / LANES;
   if (row >= static_cast<unsigned>(a.c.n_seqs) * a.M) return s;
   const unsigned b = row / static_cast<unsigned>(a.M), i = row - b * a.M;
   const int n = a.n_new ? min(__ldg(a.n_new + b), a.M) : a.M;
@@ -117,14 +119,15 @@ __device__ __forceinline__ uint32_t encode16(const Raw<__nv_bfloat16>& r, uint32
 
 // Columns col .. col + COLS - 1 of a token group: keys of heads 0 .. Hkv - 1, then values.
 template <int DH, typename T, int COLS>
-__global__ void __launch_bounds__(256) cache_write_kernel(const CacheRowsArgs a, unsigned cols) {
+__global__ void __launch_bounds__(256) cache_write_kernel(const CacheRowsArgs a, unsigned cols, unsigned warps) {
   pdl_trigger();
   pdl_wait();
   using L = cache4::Layout<DH>;
   const unsigned warp = (blockIdx.x * blockDim.x + threadIdx.x) >> 5;
+  if (warp >= warps) return;
   const unsigned group = warp / cols, col = (warp - group * cols) * COLS;
   const int blk = (threadIdx.x & 31) % (DH / cache4::kBlock);
-  const Spot s = find_spot<DH>(a, group);
+  const Spot s = find_spot<DH, 16>(a, group);
   if (!s.on) return;
   Raw<T> raw[COLS];
 #pragma unroll
@@ -145,67 +148,57 @@ __global__ void __launch_bounds__(256) cache_write_kernel(const CacheRowsArgs a,
   }
 }
 
-// 16 channels from their codes and scale byte. A nibble or-ed into the pattern of a power of two is that
+// 8 channels from their codes and scale byte. A nibble or-ed into the pattern of a power of two is that
 // plus q + 8; less that and 8, times the scale: exact.
-__device__ __forceinline__ void decode16(float* dst, uint2 w, uint32_t sb) {
-  const float sc = cache4::decode_scale(sb), less = -8388616.f * sc;  // exact: 2^20 + 1 times 8 scales
-  float x[16];
+__device__ __forceinline__ void decode8(float* dst, uint32_t w, uint32_t sb) {
+  const float sc = cache4::decode_scale(sb), less = -8388616.f * sc;  // exact: (2^20 + 1) * 15 < 2^24
+  float x[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    x[i] = fmaf(__uint_as_float(((w.x >> (4 * i)) & 15u) | 0x4B000000u), sc, less);
-    x[8 + i] = fmaf(__uint_as_float(((w.y >> (4 * i)) & 15u) | 0x4B000000u), sc, less);
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    __stcs(reinterpret_cast<float4*>(dst) + i, make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]));
-}
-__device__ __forceinline__ void decode16(__nv_bfloat16* dst, uint2 w, uint32_t sb) {
-  const __nv_bfloat162 sc = __float2bfloat162_rn(cache4::decode_scale(sb));  // 4 significant bits
-  const __nv_bfloat162 less = __float2bfloat162_rn(-136.f);                  // 128 + 8
-  uint32_t out[8];
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    uint32_t v[4];
-    const uint32_t u = h ? w.y : w.x;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {  // channels j and j + 4
-      const uint32_t n = ((u >> (4 * j)) & 0x000F000Fu) | 0x43004300u;
-      const __nv_bfloat162 q = __hmul2(__hadd2(*reinterpret_cast<const __nv_bfloat162*>(&n), less), sc);
-      v[j] = *reinterpret_cast<const uint32_t*>(&q);
-    }
-    out[4 * h] = __byte_perm(v[0], v[1], 0x5410), out[4 * h + 1] = __byte_perm(v[2], v[3], 0x5410);
-    out[4 * h + 2] = __byte_perm(v[0], v[1], 0x7632), out[4 * h + 3] = __byte_perm(v[2], v[3], 0x7632);
-  }
+  for (int i = 0; i < 8; ++i) x[i] = fmaf(__uint_as_float(((w >> (4 * i)) & 15u) | 0x4B000000u), sc, less);
 #pragma unroll
   for (int i = 0; i < 2; ++i)
-    __stcs(reinterpret_cast<uint4*>(dst) + i, make_uint4(out[4 * i], out[4 * i + 1], out[4 * i + 2], out[4 * i + 3]));
+    __stcs(reinterpret_cast<float4*>(dst) + i, make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]));
+}
+__device__ __forceinline__ void decode8(__nv_bfloat16* dst, uint32_t w, uint32_t sb) {
+  const __nv_bfloat162 sc = __float2bfloat162_rn(cache4::decode_scale(sb));  // 4 significant bits
+  const __nv_bfloat162 less = __float2bfloat162_rn(-136.f);                  // 128 + 8
+  uint32_t v[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {  // channels j and j + 4
+    const uint32_t n = ((w >> (4 * j)) & 0x000F000Fu) | 0x43004300u;
+    const __nv_bfloat162 q = __hmul2(__hadd2(*reinterpret_cast<const __nv_bfloat162*>(&n), less), sc);
+    v[j] = *reinterpret_cast<const uint32_t*>(&q);
+  }
+  __stcs(reinterpret_cast<uint4*>(dst),
+         make_uint4(__byte_perm(v[0], v[1], 0x5410), __byte_perm(v[2], v[3], 0x5410),
+                    __byte_perm(v[0], v[1], 0x7632), __byte_perm(v[2], v[3], 0x7632)));
 }
 
 template <int DH, typename T, int COLS>
-__global__ void __launch_bounds__(256) cache_read_kernel(const CacheRowsArgs a, unsigned cols) {
+__global__ void __launch_bounds__(256) cache_read_kernel(const CacheRowsArgs a, unsigned cols, unsigned warps) {
   pdl_trigger();
   pdl_wait();
   using L = cache4::Layout<DH>;
   const unsigned warp = (blockIdx.x * blockDim.x + threadIdx.x) >> 5;
+  if (warp >= warps) return;
   const unsigned group = warp / cols, col = (warp - group * cols) * COLS;
-  const int blk = (threadIdx.x & 31) % (DH / cache4::kBlock);
-  const Spot s = find_spot<DH>(a, group);
+  const int part = (threadIdx.x & 31) % (DH / 8);
+  const Spot s = find_spot<DH, 8>(a, group);
   if (!s.on) return;
-  uint2 w[COLS];
-  uint32_t sb[COLS];
+  uint32_t w[COLS], sb[COLS];
 #pragma unroll
   for (int c = 0; c < COLS; ++c) {
     const bool value = col + c >= static_cast<unsigned>(a.c.Hkv);
     const unsigned head = col + c - (value ? a.c.Hkv : 0);
     const unsigned char* half = s.page + static_cast<size_t>(head) * L::BLOCK + (value ? L::V_OFF : 0);
-    w[c] = *reinterpret_cast<const uint2*>(half + s.in_page * L::CODE_ROW + blk * 8);
-    sb[c] = half[L::CODES + s.in_page * L::SCALE_ROW + blk];
+    w[c] = *reinterpret_cast<const uint32_t*>(half + s.in_page * L::CODE_ROW + part * 4);
+    sb[c] = half[L::CODES + s.in_page * L::SCALE_ROW + part / 2];
   }
 #pragma unroll
   for (int c = 0; c < COLS; ++c) {
     const bool value = col + c >= static_cast<unsigned>(a.c.Hkv);
     const unsigned head = col + c - (value ? a.c.Hkv : 0);
-    decode16(static_cast<T*>(value ? a.v : a.k) + s.row * a.ld + head * DH + blk * cache4::kBlock, w[c], sb[c]);
+    decode8(static_cast<T*>(value ? a.v : a.k) + s.row * a.ld + head * DH + part * 8, w[c], sb[c]);
   }
 }
 
@@ -213,15 +206,16 @@ template <int DH, typename T, int COLS>
 cudaError_t launch_cols(const CacheRowsArgs& a, bool write, long long groups, cudaStream_t st) {
   const unsigned cols = 2u * a.c.Hkv / COLS;
   const long long blocks = (groups * cols + 7) / 8;
-  if (blocks > 0x0fffffffLL) return cudaErrorInvalidValue;  // the warps' numbers are 32 bits
+  if (blocks > 0x07ffffffLL) return cudaErrorInvalidValue;  // the threads' numbers are 32 bits
   const cudaError_t e = launch_pdl(write ? cache_write_kernel<DH, T, COLS> : cache_read_kernel<DH, T, COLS>,
-                                   dim3(static_cast<unsigned>(blocks)), dim3(256), 0, st, a, cols);
+                                   dim3(static_cast<unsigned>(blocks)), dim3(256), 0, st, a, cols,
+                                   static_cast<unsigned>(groups * cols));
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 template <int DH, typename T>
 cudaError_t launch_rows(const CacheRowsArgs& a, bool write, cudaStream_t st) {
-  constexpr int TOK = 32 / (DH / cache4::kBlock);
+  const int TOK = 32 / (DH / (write ? 16 : 8));  // tokens of a warp
   const long long groups = (static_cast<long long>(a.c.n_seqs) * a.M + TOK - 1) / TOK;
   // four columns a warp once that leaves every SM its 64 warps
   if (a.c.Hkv % 2 == 0 && groups * 2 * a.c.Hkv / 4 >= 148 * 64) return launch_cols<DH, T, 4>(a, write, groups, st);
