@@ -325,6 +325,36 @@ def run_microbench(args, local: int) -> int:
             emit("attention", {"G": G, "M": M, "H": H, "Hkv": Hkv, "dh": dh}, ms,
                  G * H * 4.0 * dh * M * (M + 1) / 2, "TFLOP/s", peaks["bf16_tflops"], "bf16_tflops")
             del qkv, out
+        # the same heads over a window with sinks, in the segments and in one long prompt; flops of the
+        # visible (query, key) pairs
+        for G, M, window, sinks in ((16, 1040, 256, 16), (1, 65536, 1024, 4)):
+            qkv = (torch.randn(G, M, (H + 2 * Hkv) * dh, device=dev, generator=gen) * 0.5).to(torch.bfloat16)
+            out = torch.empty(G, M, H * dh, device=dev, dtype=torch.bfloat16)
+            ms = median_ms(lambda: rmt.rmt_attention_window(qkv, out, G, M, H, Hkv, dh, window, sinks))
+            seen = sum(min(i + 1, window) + max(0, min(sinks, i + 1 - window)) for i in range(M))
+            emit("attention_window", {"G": G, "M": M, "H": H, "Hkv": Hkv, "dh": dh, "window": window, "sinks": sinks},
+                 ms, G * H * 4.0 * dh * seen, "TFLOP/s", peaks["bf16_tflops"], "bf16_tflops")
+            del qkv, out
+        # the 4-bit key/value cache: a prompt written and read back, then one token of each sequence over it;
+        # bytes of the rows and of the codes and scales
+        for n, T in ((64, 4096), (1, 131072)):
+            per = T // rmt.RMT_CACHE_PAGE
+            pages = torch.zeros(n * per, Hkv, 72 * dh, device=dev, dtype=torch.uint8)
+            table = torch.randperm(n * per, device=dev, generator=gen).to(torch.int32).reshape(n, per)
+            cache = rmt.rmt_cache(pages, table, torch.full((n,), T, device=dev, dtype=torch.int32), Hkv, dh)
+            k, v = (torch.randn(n, T, Hkv * dh, device=dev, generator=gen).to(torch.bfloat16) for _ in range(2))
+            rows, held = 2 * k.numel() * 2, 2 * k.numel() * 9 // 16
+            cfg = {"sequences": n, "tokens": T, "H": H, "Hkv": Hkv, "dh": dh}
+            ms = median_ms(lambda: rmt.rmt_cache_write(cache, k, v, T))
+            emit("cache_write", cfg, ms, rows + held, "GB/s", peaks["hbm_gbs"], "hbm_gbs")
+            ms = median_ms(lambda: rmt.rmt_cache_read(cache, k, v, T))
+            emit("cache_read", cfg, ms, rows + held, "GB/s", peaks["hbm_gbs"], "hbm_gbs")
+            q = torch.randn(n, 1, H * dh, device=dev, generator=gen).to(torch.bfloat16)
+            out = torch.empty_like(q)
+            ws = torch.empty(rmt.rmt_attention_cache_workspace(cache, 1, H), device=dev, dtype=torch.uint8)
+            ms = median_ms(lambda: rmt.rmt_attention_cache(cache, q, out, 1, H, 0, 0, ws))
+            emit("attention_cache", cfg, ms, held + 4 * q.numel(), "GB/s", peaks["hbm_gbs"], "hbm_gbs")
+            del pages, table, cache, k, v, q, out, ws
         return 0
 
     # memory-path kernels: the diagonal's size (G = 16 cells) and about 10^6 rows (HBM-bound)
