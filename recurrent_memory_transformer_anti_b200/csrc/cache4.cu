@@ -1,14 +1,17 @@
 // Writing rows into the 4-bit key/value cache, and reading them back (layout and arithmetic:
 // cache4.cuh). Both stream. Writing, a thread holds the 16 channels of one scale, so a block's maximum
-// needs no other lane and a scale is worked out once (8 channels a thread and an exchange: 26 us instead
-// of 22 for 67 MB of bf16); reading, it holds 8 channels, 16 bytes of bf16, so that each
-// store of a warp fills whole sectors (16 channels a thread: 22 us instead of 15). A warp takes
-// four (keys or values, head) columns of its tokens where there are warps enough, with their loads in
-// flight together and the tokens' pages looked up once.
+// needs no other lane and a scale is worked out once (8 channels a thread and an exchange between two: 45 us
+// for the write and read of the 153 MB below instead of 37); reading, it holds 8 channels, 16 bytes
+// of bf16, so that each store of a warp fills whole sectors (16 channels: 33.0 us instead of 26.5 for 136 MB).
+// A warp takes four neighbouring heads of its tokens where there are warps enough: their loads in flight
+// together, their tokens' pages looked up once, and one address for all, the rest being constants.
 //
-// Bound by HBM if the arithmetic stays at about 5 instructions a channel: a bf16 channel is
-// rounded in two (encode_short); blocks with a NaN, a saturating value or a scale below 2^-14, and fp32,
-// take the general way (encode_value).
+// Bound by HBM if the arithmetic stays at about 5 instructions a channel: a bf16 channel is rounded in
+// half a packed operation twice (encode_short), read in one and a half (decode8), and places are found
+// without a division. Blocks with a NaN, a saturating value or a scale below 2^-14, and fp32, take the
+// general way (encode_value). bf16 rows of 8 heads: 67 MB into 19 MB of codes and scales take 15.8 us
+// (5.4 TB/s), 30 MB into 106 MB 25.4 us (5.4 TB/s). What is left is the chain of three loads (length, page,
+// codes) at the head of each wave of CTAs.
 #include "cache4.cuh"
 #include "launch.h"
 
@@ -17,30 +20,48 @@ namespace {
 
 using cache4::kPage;
 
-// Where this thread's token is: its row of k and v, and its page.
+// n / d of numbers below 2^31: (n * m) >> s, m = 2^s / d rounded up and below 2^32 + 1, so that what
+// rounding adds, n / 2^s at most, does not reach the next integer.
+struct Divider {
+  uint32_t m;
+  int s;
+  explicit Divider(uint32_t d) : s(31) {
+    while ((uint64_t(1) << (s - 31)) < d) ++s;
+    m = static_cast<uint32_t>(((uint64_t(1) << s) + d - 1) / d);
+  }
+  __device__ __forceinline__ uint32_t operator()(uint32_t n) const {
+    return static_cast<uint32_t>((static_cast<uint64_t>(n) * m) >> s);
+  }
+};
+
+// What a launch adds to its arguments: a warp's columns are COLS neighbouring heads of keys or of values,
+// `cols` such ranges for both, and `warps` of them in all.
+struct Deal {
+  uint32_t cols, warps;
+  Divider by_cols, by_m;
+};
+
+// Where this thread's token is: its row of k and v, and the table's page for it.
 struct Spot {
   bool on;
   size_t row;
-  unsigned char* page;
-  int in_page;
+  int page, in_page;
 };
 
 // CH: channels of a thread
 template <int DH, int CH>
-__device__ __forceinline__ Spot find_spot(const CacheRowsArgs& a, unsigned group) {
-  constexpr unsigned LANES = DH / CH, TOK = 32 / LANES;
+__device__ __forceinline__ Spot find_spot(const CacheRowsArgs& a, const Deal& d, uint32_t group) {
+  constexpr uint32_t LANES = DH / CH, TOK = 32 / LANES;
   Spot s{};
-  const unsigned row = group * TOK + (threadIdx.x & 31u) / LANES;
-  if (row >= static_cast<unsigned>(a.c.n_seqs) * a.M) return s;
-  const unsigned b = row / static_cast<unsigned>(a.M), i = row - b * a.M;
+  const uint32_t row = group * TOK + (threadIdx.x & 31u) / LANES;
+  if (row >= static_cast<uint32_t>(a.c.n_seqs) * a.M) return s;
+  const uint32_t b = d.by_m(row), i = row - b * a.M;
   const int n = a.n_new ? min(__ldg(a.n_new + b), a.M) : a.M;
   const int pos = __ldg(a.c.lens + b) - n + static_cast<int>(i);
   if (static_cast<int>(i) >= n || pos < 0) return s;  // past the sequence's new rows, or of an empty slot
-  const int page = cache4::page_of(a.c, b, pos);
-  if (page < 0) return s;
   s.on = true;
   s.row = row;
-  s.page = a.c.pages + cache4::block_offset<DH>(a.c, page, 0);
+  s.page = cache4::table_entry(a.c, b, pos);
   s.in_page = pos % kPage;
   return s;
 }
@@ -94,20 +115,25 @@ __device__ __forceinline__ uint32_t encode16(const Raw<__nv_bfloat16>& r, uint32
 #pragma unroll
   for (int i = 1; i < 8; ++i) m = __hmax2_nan(m, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[i])));
   const float amax = __bfloat162float(__hmax_nan(m.x, m.y));
-  float x[16];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    x[2 * i] = __uint_as_float(w[i] << 16);
-    x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-  }
-  const uint32_t sb = cache4::encode_scale(amax);
-  // short way: scales from 2^-14 on (within 1/16 of max / 7, so quotients stay below 7.5), no
-  // saturation, no NaN
-  if (!(amax <= cache4::kAmax) || sb < 8) return encode_general(x, lo, hi);
-  const float rs = 1.f / cache4::decode_scale(sb);
   uint32_t u[16];
 #pragma unroll
-  for (int i = 0; i < 16; ++i) u[i] = cache4::encode_short(x[i], rs);
+  for (int i = 0; i < 8; ++i) {
+    u[2 * i] = w[i] << 16;
+    u[2 * i + 1] = w[i] & 0xFFFF0000u;
+  }
+  // short way: scales from 2^-14 on (within 1/16 of max / 7, so quotients stay below 7.5), no
+  // saturation, no NaN
+  if (!(amax >= 7.f * 6.103515625e-05f && amax <= cache4::kAmax)) {
+    float x[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) x[i] = __uint_as_float(u[i]);
+    return encode_general(x, lo, hi);
+  }
+  const uint32_t sb = cache4::encode_scale_short(amax);
+  float rs;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(rs) : "f"(cache4::decode_scale(sb)));  // off by one step at most
+#pragma unroll
+  for (int i = 0; i < 16; i += 2) cache4::encode_short(u[i], u[i + 1], rs);
   // low bytes: even channels, then odd ones in the high nibbles
   auto bytes = [](uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
     return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
@@ -117,34 +143,36 @@ __device__ __forceinline__ uint32_t encode16(const Raw<__nv_bfloat16>& r, uint32
   return sb;
 }
 
-// Columns col .. col + COLS - 1 of a token group: keys of heads 0 .. Hkv - 1, then values.
 template <int DH, typename T, int COLS>
-__global__ void __launch_bounds__(256) cache_write_kernel(const CacheRowsArgs a, unsigned cols, unsigned warps) {
+__global__ void __launch_bounds__(256) cache_write_kernel(const CacheRowsArgs a, const Deal d) {
   pdl_trigger();
   pdl_wait();
   using L = cache4::Layout<DH>;
-  const unsigned warp = (blockIdx.x * blockDim.x + threadIdx.x) >> 5;
-  if (warp >= warps) return;
-  const unsigned group = warp / cols, col = (warp - group * cols) * COLS;
+  const uint32_t warp = (blockIdx.x * blockDim.x + threadIdx.x) >> 5;
+  if (warp >= d.warps) return;
+  const uint32_t group = d.by_cols(warp);
+  uint32_t head = (warp - group * d.cols) * COLS;
+  const bool value = head >= static_cast<uint32_t>(a.c.Hkv);
+  if (value) head -= a.c.Hkv;
   const int blk = (threadIdx.x & 31) % (DH / cache4::kBlock);
-  const Spot s = find_spot<DH, 16>(a, group);
+  const Spot s = find_spot<DH, 16>(a, d, group);
   if (!s.on) return;
+  // the rows' loads go out before the page's number is looked at
+  const T* const src = static_cast<const T*>(value ? a.v : a.k) + s.row * a.ld + head * DH + blk * cache4::kBlock;
   Raw<T> raw[COLS];
 #pragma unroll
-  for (int c = 0; c < COLS; ++c) {
-    const bool value = col + c >= static_cast<unsigned>(a.c.Hkv);
-    const unsigned head = col + c - (value ? a.c.Hkv : 0);
-    raw[c] = load16(static_cast<const T*>(value ? a.v : a.k) + s.row * a.ld + head * DH + blk * cache4::kBlock);
-  }
+  for (int c = 0; c < COLS; ++c) raw[c] = load16(src + c * DH);
+  if (!cache4::page_ok(a.c, s.page)) return;
+  unsigned char* const half =
+      a.c.pages + cache4::block_offset<DH>(a.c, s.page, head) + (value ? L::V_OFF : 0);
+  unsigned char* const codes = half + s.in_page * L::CODE_ROW + blk * 8;
+  unsigned char* const scale = half + L::CODES + s.in_page * L::SCALE_ROW + blk;
 #pragma unroll
   for (int c = 0; c < COLS; ++c) {
-    const bool value = col + c >= static_cast<unsigned>(a.c.Hkv);
-    const unsigned head = col + c - (value ? a.c.Hkv : 0);
     uint32_t lo, hi;
     const uint32_t sb = encode16(raw[c], lo, hi);
-    unsigned char* half = s.page + static_cast<size_t>(head) * L::BLOCK + (value ? L::V_OFF : 0);
-    *reinterpret_cast<uint2*>(half + s.in_page * L::CODE_ROW + blk * 8) = make_uint2(lo, hi);
-    half[L::CODES + s.in_page * L::SCALE_ROW + blk] = static_cast<unsigned char>(sb);
+    *reinterpret_cast<uint2*>(codes + c * L::BLOCK) = make_uint2(lo, hi);
+    scale[c * L::BLOCK] = static_cast<unsigned char>(sb);
   }
 }
 
@@ -159,57 +187,60 @@ __device__ __forceinline__ void decode8(float* dst, uint32_t w, uint32_t sb) {
   for (int i = 0; i < 2; ++i)
     __stcs(reinterpret_cast<float4*>(dst) + i, make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]));
 }
+// In bf16: the bits 0..15 of a nibble are l * 2^-133, which times 2^120 less 8 * 2^-13 is q * 2^-13; the
+// scale's byte, four bits up, is 2^-112 of the scale, which times 2^125 is 2^13 of it. All exact.
 __device__ __forceinline__ void decode8(__nv_bfloat16* dst, uint32_t w, uint32_t sb) {
-  const __nv_bfloat162 sc = __float2bfloat162_rn(cache4::decode_scale(sb));  // 4 significant bits
-  const __nv_bfloat162 less = __float2bfloat162_rn(-136.f);                  // 128 + 8
+  auto pair = [](uint32_t u) { return *reinterpret_cast<const __nv_bfloat162*>(&u); };
+  const __nv_bfloat162 sc = __hmul2(pair(sb * 0x00100010u), pair(0x7E007E00u));  // 2^125
+  const uint32_t even = w & 0x0F0F0F0Fu, odd = (w >> 4) & 0x0F0F0F0Fu;
   uint32_t v[4];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {  // channels j and j + 4
-    const uint32_t n = ((w >> (4 * j)) & 0x000F000Fu) | 0x43004300u;
-    const __nv_bfloat162 q = __hmul2(__hadd2(*reinterpret_cast<const __nv_bfloat162*>(&n), less), sc);
+  for (int j = 0; j < 4; ++j) {  // channels 2 j and 2 j + 1: byte j of each, in the low byte of a half
+    uint32_t n;  // selectors with their top bit set fill a byte with the named byte's sign, here 0
+    asm("prmt.b32 %0, %1, %2, %3;" : "=r"(n) : "r"(even), "r"(odd), "r"(0xC480u + 0x1111u * j));
+    const __nv_bfloat162 q = __hmul2(__hfma2(pair(n), pair(0x7B807B80u), pair(0xBA80BA80u)), sc);
     v[j] = *reinterpret_cast<const uint32_t*>(&q);
   }
-  __stcs(reinterpret_cast<uint4*>(dst),
-         make_uint4(__byte_perm(v[0], v[1], 0x5410), __byte_perm(v[2], v[3], 0x5410),
-                    __byte_perm(v[0], v[1], 0x7632), __byte_perm(v[2], v[3], 0x7632)));
+  __stcs(reinterpret_cast<uint4*>(dst), make_uint4(v[0], v[1], v[2], v[3]));
 }
 
 template <int DH, typename T, int COLS>
-__global__ void __launch_bounds__(256) cache_read_kernel(const CacheRowsArgs a, unsigned cols, unsigned warps) {
+__global__ void __launch_bounds__(256) cache_read_kernel(const CacheRowsArgs a, const Deal d) {
   pdl_trigger();
   pdl_wait();
   using L = cache4::Layout<DH>;
-  const unsigned warp = (blockIdx.x * blockDim.x + threadIdx.x) >> 5;
-  if (warp >= warps) return;
-  const unsigned group = warp / cols, col = (warp - group * cols) * COLS;
+  const uint32_t warp = (blockIdx.x * blockDim.x + threadIdx.x) >> 5;
+  if (warp >= d.warps) return;
+  const uint32_t group = d.by_cols(warp);
+  uint32_t head = (warp - group * d.cols) * COLS;
+  const bool value = head >= static_cast<uint32_t>(a.c.Hkv);
+  if (value) head -= a.c.Hkv;
   const int part = (threadIdx.x & 31) % (DH / 8);
-  const Spot s = find_spot<DH, 8>(a, group);
-  if (!s.on) return;
+  const Spot s = find_spot<DH, 8>(a, d, group);
+  if (!s.on || !cache4::page_ok(a.c, s.page)) return;
+  const unsigned char* const half =
+      a.c.pages + cache4::block_offset<DH>(a.c, s.page, head) + (value ? L::V_OFF : 0);
+  const unsigned char* const codes = half + s.in_page * L::CODE_ROW + part * 4;
+  const unsigned char* const scale = half + L::CODES + s.in_page * L::SCALE_ROW + part / 2;
   uint32_t w[COLS], sb[COLS];
 #pragma unroll
   for (int c = 0; c < COLS; ++c) {
-    const bool value = col + c >= static_cast<unsigned>(a.c.Hkv);
-    const unsigned head = col + c - (value ? a.c.Hkv : 0);
-    const unsigned char* half = s.page + static_cast<size_t>(head) * L::BLOCK + (value ? L::V_OFF : 0);
-    w[c] = *reinterpret_cast<const uint32_t*>(half + s.in_page * L::CODE_ROW + part * 4);
-    sb[c] = half[L::CODES + s.in_page * L::SCALE_ROW + part / 2];
+    w[c] = *reinterpret_cast<const uint32_t*>(codes + c * L::BLOCK);
+    sb[c] = scale[c * L::BLOCK];
   }
+  T* const dst = static_cast<T*>(value ? a.v : a.k) + s.row * a.ld + head * DH + part * 8;
 #pragma unroll
-  for (int c = 0; c < COLS; ++c) {
-    const bool value = col + c >= static_cast<unsigned>(a.c.Hkv);
-    const unsigned head = col + c - (value ? a.c.Hkv : 0);
-    decode8(static_cast<T*>(value ? a.v : a.k) + s.row * a.ld + head * DH + part * 8, w[c], sb[c]);
-  }
+  for (int c = 0; c < COLS; ++c) decode8(dst + c * DH, w[c], sb[c]);
 }
 
 template <int DH, typename T, int COLS>
 cudaError_t launch_cols(const CacheRowsArgs& a, bool write, long long groups, cudaStream_t st) {
-  const unsigned cols = 2u * a.c.Hkv / COLS;
+  const uint32_t cols = 2u * a.c.Hkv / COLS;
   const long long blocks = (groups * cols + 7) / 8;
   if (blocks > 0x07ffffffLL) return cudaErrorInvalidValue;  // the threads' numbers are 32 bits
+  const Deal d{cols, static_cast<uint32_t>(groups * cols), Divider(cols), Divider(a.M)};
   const cudaError_t e = launch_pdl(write ? cache_write_kernel<DH, T, COLS> : cache_read_kernel<DH, T, COLS>,
-                                   dim3(static_cast<unsigned>(blocks)), dim3(256), 0, st, a, cols,
-                                   static_cast<unsigned>(groups * cols));
+                                   dim3(static_cast<unsigned>(blocks)), dim3(256), 0, st, a, d);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
@@ -217,8 +248,12 @@ template <int DH, typename T>
 cudaError_t launch_rows(const CacheRowsArgs& a, bool write, cudaStream_t st) {
   const int TOK = 32 / (DH / (write ? 16 : 8));  // tokens of a warp
   const long long groups = (static_cast<long long>(a.c.n_seqs) * a.M + TOK - 1) / TOK;
-  // four columns a warp once that leaves every SM its 64 warps
-  if (a.c.Hkv % 2 == 0 && groups * 2 * a.c.Hkv / 4 >= 148 * 64) return launch_cols<DH, T, 4>(a, write, groups, st);
+  // Four (or two) heads a warp once that leaves every SM 16 warps. With 8 heads of 64 in bf16, of
+  // four heads and of one: a write of 4096 tokens (14 warps an SM with four) takes 4.1 and 3.7 us, of 8192 4.7 and
+  // 5.5; a read of 512 (4 warps) 2.25 and 2.05, of 4096 (28 warps) 3.7 and 4.1, of 65,536 27 and 43.
+  const long long enough = 148 * 16;
+  if (a.c.Hkv % 4 == 0 && groups * 2 * a.c.Hkv / 4 >= enough) return launch_cols<DH, T, 4>(a, write, groups, st);
+  if (a.c.Hkv % 2 == 0 && groups * 2 * a.c.Hkv / 2 >= enough) return launch_cols<DH, T, 2>(a, write, groups, st);
   return launch_cols<DH, T, 1>(a, write, groups, st);
 }
 

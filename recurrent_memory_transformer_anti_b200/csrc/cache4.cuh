@@ -40,17 +40,16 @@ struct CacheArgs {
   int* err;
 };
 
-// Page of token `pos` of sequence b, or -1 (and kErrPage in the error word) when the table or the
-// position does not fit the cache: the caller then makes no access.
-__device__ __forceinline__ int page_of(const CacheArgs& c, int b, int pos) {
+// Page of token `pos` of sequence b as the table has it, -1 for a position that does not fit it.
+__device__ __forceinline__ int table_entry(const CacheArgs& c, int b, int pos) {
   const int slot = pos / kPage;
-  int page = -1;
-  if (pos >= 0 && slot < c.max_pages) page = __ldg(c.table + static_cast<size_t>(b) * c.max_pages + slot);
-  if (page < 0 || page >= c.n_pages) {
-    if (c.err) atomicOr(c.err, kErrPage);
-    return -1;
-  }
-  return page;
+  return pos >= 0 && slot < c.max_pages ? __ldg(c.table + static_cast<size_t>(b) * c.max_pages + slot) : -1;
+}
+// Whether that is a page of the cache; if not, kErrPage goes to the error word, and the caller makes no access.
+__device__ __forceinline__ bool page_ok(const CacheArgs& c, int page) {
+  if (page >= 0 && page < c.n_pages) return true;
+  if (c.err) atomicOr(c.err, kErrPage);
+  return false;
 }
 
 template <int DH>
@@ -89,12 +88,26 @@ __device__ __forceinline__ uint32_t encode_value(float x, float s, float rs) {
   return static_cast<uint32_t>(static_cast<int>(q) + 8);
 }
 
-// encode_value for a bf16 x and a scale whose quotients stay below 7.5 in magnitude: q + 8 in the low byte.
+// encode_scale for amax a bf16 in [7 * 2^-14, kAmax]. It has 8 significant bits, so amax / 7 is halfway
+// between two scales or at least 2^-9 of its value off: the product with 1 / 7, two steps of 2^-23 off
+// at most, rounded to 15 mantissa bits, is halfway when the quotient is.
+__device__ __forceinline__ uint32_t encode_scale_short(float amax) {
+  const uint32_t v = (__float_as_uint(amax * (1.f / 7.f)) + 0x80u) >> 8;
+  return ((v + 0x7FFu + ((v >> 12) & 1u)) >> 12) - (112u << 3);
+}
+
+// encode_value for two bf16 x and a scale whose quotients stay below 7.5 in magnitude: q + 8 in the low byte.
 // x and s have 8 and 4 significant bits, so x / s is a tie or at least 2^-12 off one: rounding
-// x * rs, which is within 2^-22 of it, to steps of 2^-14 puts the ties back where they belong, and
-// the second sum rounds to the nearest integer. Its constant is 1.5 * 2^23 + 8 less the first's 1.5 * 2^9.
-__device__ __forceinline__ uint32_t encode_short(float x, float rs) {
-  return __float_as_uint(fmaf(x, rs, 768.f) + 12582152.f);
+// x * rs, which is within 2^-18 of it (rs within 2^-22 of 1 / s), to steps of 2^-14 puts the ties back
+// where they belong, and the second sum rounds to the nearest integer. Its constant is 1.5 * 2^23 + 8
+// less the first's 1.5 * 2^9.
+__device__ __forceinline__ void encode_short(uint32_t& x0, uint32_t& x1, float rs) {
+  asm("{\n\t.reg .b64 x, y, z;\n\t"
+      "mov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %2};\n\tmov.b64 z, {%3, %3};\n\t"
+      "fma.rn.f32x2 x, x, y, z;\n\tmov.b64 z, {%4, %4};\n\tadd.rn.f32x2 x, x, z;\n\t"
+      "mov.b64 {%0, %1}, x;\n\t}"
+      : "+r"(x0), "+r"(x1)
+      : "f"(rs), "f"(768.f), "f"(12582152.f));
 }
 
 }  // namespace cache4

@@ -209,6 +209,36 @@ def test_write_of_special_values_and_ties(cuda_ok, dtype):
 
 
 @gpu
+@pytest.mark.parametrize("Hkv", [4, 2])
+def test_write_and_read_of_every_bf16_as_a_blocks_largest(cuda_ok, Hkv):
+    """Each non-negative bf16 but NaN as the largest of 16 channels, the others at halves of its steps and between;
+    the same rows again and again until a launch takes several heads a warp."""
+    dh, per = 128, Hkv * 8
+    r = np.random.default_rng(5)
+    top = torch.arange(0x7F81, dtype=torch.int16).view(torch.bfloat16).double().numpy()
+    top = np.concatenate((top, np.full(-len(top) % per, 1.0)))
+    scale = SCALES[encode_ref(np.repeat(top, 16)[None])[1][0]]
+    q = np.concatenate((np.arange(-7, 8) + 0.5 * r.choice([-1, 1], 15), [0.0]))[:15]
+    x = np.concatenate((top[:, None], scale[:, None] * (q + r.choice([0.0, 0.25], (len(top), 15)))), 1)
+    x[:, 1:] = np.clip(x[:, 1:], -top[:, None], top[:, None])
+    x = torch.tensor(x.reshape(1, -1, Hkv * dh)).bfloat16()
+    want = decode_ref(*encode_ref(x.double().numpy()))[0]
+    rows = x.shape[1]
+    times = -(-20000 // rows)
+    k = x.cuda().repeat(1, times, 1)
+    v = k.flip(1)
+    M = k.shape[1]
+    s = Setup([M], Hkv, dh)
+    rmt.rmt_cache_write(s.cache, k, v, M)
+    ko, vo = torch.zeros_like(k), torch.zeros_like(v)
+    rmt.rmt_cache_read(s.cache, ko, vo, M)
+    rmt.rmt_sync(None)
+    for got in (ko[0], vo[0].flip(0)):
+        np.testing.assert_array_equal(f64(got[:rows]), want)
+        assert torch.equal(got.view(times, rows, -1), got[:rows].expand(times, -1, -1))
+
+
+@gpu
 def test_lengths_and_pages_that_do_not_fit_are_reported_and_skipped(cuda_ok):
     dh, Hkv, H = 64, 2, 4
     s = Setup([130, 64, 100], Hkv, dh, fill=0)
