@@ -1,28 +1,33 @@
 // Attention over a sliding window and the first tokens (sinks), fp32 FMA: row i of a sequence sees
 // the keys j <= i with i - j < window or j < sinks.
 //
-// A CTA of 128 threads holds 64 query rows of one head and passes over the keys they can see in
-// tiles of 64: the tiles of the sinks, then those of the window, from the first row's oldest key
-// to the last row's own. Each thread keeps 8 queries x 4 keys of the scores and 8 queries x dh/16
-// channels of the output in registers; a row's maximum and sum run along (one pass over the keys).
+// A CTA of 128 threads holds 8 NQ query rows of one head (32, or 16 in calls of few rows) and passes
+// over the keys they can see in tiles of 64: the sinks, then the window from the first row's oldest key
+// to the last row's own, numbered u = 0, 1, .. without a gap. Each thread keeps NQ queries x 4 keys of the
+// scores and NQ queries x dh/16 channels of the output in registers; a row's maximum and sum run along
+// (one pass over the keys).
 // Key rows past the sequence's end are never read. A weight of zero adds nothing even when the
 // value it belongs to is not finite, so what is masked cannot reach a row.
-// Bound by the fp32 FMA pipe and the shared-memory reads that feed it. Serves fp32, and bf16 heads
-// of 32 (bf16 heads of 64 and 128: attention_window_tc.cu).
+// Bound by the fp32 FMA pipe and the shared-memory reads that feed it: 16 bytes at a time, 8 of them for
+// 64 FMA. Two sequences of 1040 rows, 32 / 8 heads of 64, window 256, 16 sinks: 161 us, 25 TFLOP/s of
+// what is visible; two of 208 rows with 4 / 2 heads, window 64, which only fill the SMs with 16 rows a CTA: 8.6 us.
+// Serves fp32, and bf16 heads of 32 (bf16 heads of 64 and 128: attention_window_tc.cu).
 #include "cache4.cuh"
 #include "launch.h"
 
 namespace rmt {
 namespace {
 
-template <int DH>
+// Shared memory: rows padded by 16 bytes, so that eight rows' reads of 16 bytes at one column touch all banks.
+template <int DH, int NQ>
 struct WinSimt {
-  static constexpr int BQ = 64, BK = 64, PAD = 4;
-  static constexpr int Q_OFF = 0;                        // [dh][BQ + PAD], scaled
-  static constexpr int K_OFF = Q_OFF + DH * (BQ + PAD);  // [dh][BK + PAD]
-  static constexpr int V_OFF = K_OFF + DH * (BK + PAD);  // [BK][dh]
-  static constexpr int P_OFF = V_OFF + BK * DH;          // [BK][BQ + PAD]
-  static constexpr int BYTES = (P_OFF + BK * (BQ + PAD)) * 4;
+  static constexpr int BQ = 8 * NQ, BK = 64;
+  static constexpr int LD = DH + 4, LP = BK + 4;
+  static constexpr int Q_OFF = 0;                    // [BQ][LD], scaled
+  static constexpr int K_OFF = Q_OFF + BQ * LD;      // [BK][LD]
+  static constexpr int V_OFF = K_OFF + BK * LD;      // [BK][LD]
+  static constexpr int P_OFF = V_OFF + BK * LD;      // [BQ][LP]
+  static constexpr int BYTES = (P_OFF + BQ * LP) * 4;
 };
 
 __device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
@@ -32,12 +37,27 @@ __device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
                      __uint_as_float(u.y & 0xFFFF0000u));
 }
 
-template <int DH, typename T>
+// N consecutive floats
+template <int N>
+__device__ __forceinline__ void lds(const float* p, float (&v)[N]) {
+  if constexpr (N == 2) {
+    const float2 f = *reinterpret_cast<const float2*>(p);
+    v[0] = f.x, v[1] = f.y;
+  } else {
+#pragma unroll
+    for (int c = 0; c < N; c += 4) {
+      const float4 f = *reinterpret_cast<const float4*>(p + c);
+      v[c] = f.x, v[c + 1] = f.y, v[c + 2] = f.z, v[c + 3] = f.w;
+    }
+  }
+}
+
+template <int DH, typename T, int NQ>
 __global__ void __launch_bounds__(128) window_simt_kernel(const WindowAttnArgs a) {
   pdl_trigger();
   pdl_wait();
-  using S = WinSimt<DH>;
-  constexpr int BQ = S::BQ, BK = S::BK, LQ = BQ + S::PAD, LK = BK + S::PAD, NC = DH / 16;
+  using S = WinSimt<DH, NQ>;
+  constexpr int BQ = S::BQ, BK = S::BK, LD = S::LD, LP = S::LP, NC = DH / 16;
   extern __shared__ float sm[];
   float *Qs = sm + S::Q_OFF, *Ks = sm + S::K_OFF, *Vs = sm + S::V_OFF, *Ps = sm + S::P_OFF;
   const int h = blockIdx.y, g = blockIdx.z, t = threadIdx.x;
@@ -47,18 +67,18 @@ __global__ void __launch_bounds__(128) window_simt_kernel(const WindowAttnArgs a
   const int kvh = h / (a.H / a.Hkv);
   const size_t ld = static_cast<size_t>(a.H + 2 * a.Hkv) * DH;
   const T* base = static_cast<const T*>(a.qkv) + static_cast<size_t>(g) * a.M * ld;
-  const int ty = t >> 4, tx = t & 15;  // queries 8 ty .., keys tx + 16 e, channels NC tx ..
+  const int ty = t >> 4, tx = t & 15;  // queries NQ ty .., keys tx + 16 e, channels NC tx ..
   const float scale = rsqrtf(static_cast<float>(DH)) * 1.4426950408889634f;  // scores in powers of 2
 
-  for (int e = t; e < BQ * (DH / 4); e += 128) {
-    const int r = e % BQ, c = (e / BQ) * 4, row = q0 + r;
-    const float4 v = row < len ? load4(base + row * ld + h * DH + c) : make_float4(0.f, 0.f, 0.f, 0.f);
-    Qs[c * LQ + r] = v.x * scale, Qs[(c + 1) * LQ + r] = v.y * scale;
-    Qs[(c + 2) * LQ + r] = v.z * scale, Qs[(c + 3) * LQ + r] = v.w * scale;
-  }
-  float o[8][NC], m[8], l[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < BQ * (DH / 4) / 128; ++i) {
+    const int e = t + 128 * i, r = e / (DH / 4), c = (e % (DH / 4)) * 4, row = q0 + r;
+    const float4 v = row < len ? load4(base + row * ld + h * DH + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+    *reinterpret_cast<float4*>(Qs + r * LD + c) = make_float4(v.x * scale, v.y * scale, v.z * scale, v.w * scale);
+  }
+  float o[NQ][NC], m[NQ], l[NQ];
+#pragma unroll
+  for (int i = 0; i < NQ; ++i) {
     m[i] = -INFINITY;
     l[i] = 0.f;
 #pragma unroll
@@ -66,54 +86,61 @@ __global__ void __launch_bounds__(128) window_simt_kernel(const WindowAttnArgs a
   }
   const int qlast = min(q0 + BQ, len) - 1;
   const int lo = max(0, q0 - a.window + 1);     // oldest key of the first row's window
-  const int sink_end = min(a.sinks, lo);        // sinks not already in it
-  const int n_sink = (sink_end + BK - 1) / BK;  // their tiles start at 0, the window's at lo
-  const int n_win = (qlast - lo) / BK + 1;
-  for (int tile = 0; tile < n_sink + n_win; ++tile) {
-    const bool in_sink = tile < n_sink;
-    const int k0 = in_sink ? tile * BK : lo + (tile - n_sink) * BK;
-    const int kend = in_sink ? sink_end : qlast + 1;  // keys of this tile end here
-    __syncthreads();
-    for (int e = t; e < BK * (DH / 4); e += 128) {
-      const int r = e % BK, c = (e / BK) * 4, row = k0 + r;
-      const float4 v = row < kend ? load4(base + row * ld + (a.H + kvh) * DH + c) : make_float4(0.f, 0.f, 0.f, 0.f);
-      Ks[c * LK + r] = v.x, Ks[(c + 1) * LK + r] = v.y, Ks[(c + 2) * LK + r] = v.z, Ks[(c + 3) * LK + r] = v.w;
-    }
-    for (int e = t; e < BK * (DH / 4); e += 128) {
-      const int c = (e % (DH / 4)) * 4, r = e / (DH / 4), row = k0 + r;
-      const float4 v =
-          row < kend ? load4(base + row * ld + (a.H + a.Hkv + kvh) * DH + c) : make_float4(0.f, 0.f, 0.f, 0.f);
-      *reinterpret_cast<float4*>(Vs + r * DH + c) = v;
-    }
-    __syncthreads();
-    float s[8][4];
+  const int sinks = min(a.sinks, lo);           // those not already in it
+  const int keys = sinks + qlast - lo + 1;
+  auto key_of = [&](int u) { return u < sinks ? u : lo + u - sinks; };
+  for (int u0 = 0; u0 < keys; u0 += BK) {
+    // a tile's loads in flight together
+    constexpr int PER = BK * (DH / 4) / 128;
+    float4 kr[PER], vr[PER];
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < PER; ++i) {
+      const int e = t + 128 * i, u = u0 + e / (DH / 4), c = (e % (DH / 4)) * 4;
+      kr[i] = vr[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (u < keys) {
+        const T* const p = base + key_of(u) * ld + (a.H + kvh) * DH + c;
+        kr[i] = load4(p);
+        vr[i] = load4(p + a.Hkv * DH);
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int e = t + 128 * i, at = e / (DH / 4) * LD + (e % (DH / 4)) * 4;
+      *reinterpret_cast<float4*>(Ks + at) = kr[i];
+      *reinterpret_cast<float4*>(Vs + at) = vr[i];
+    }
+    __syncthreads();
+    float s[NQ][4];
+#pragma unroll
+    for (int i = 0; i < NQ; ++i)
 #pragma unroll
       for (int e = 0; e < 4; ++e) s[i][e] = 0.f;
-#pragma unroll 8
-    for (int d = 0; d < DH; ++d) {
-      const float4 qa = *reinterpret_cast<const float4*>(Qs + d * LQ + 8 * ty);
-      const float4 qb = *reinterpret_cast<const float4*>(Qs + d * LQ + 8 * ty + 4);
-      const float qv[8] = {qa.x, qa.y, qa.z, qa.w, qb.x, qb.y, qb.z, qb.w};
-      float kv[4];
+#pragma unroll 4
+    for (int d = 0; d < DH; d += 4) {
+      float qv[NQ][4], kv[4][4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) kv[e] = Ks[d * LK + tx + 16 * e];
+      for (int i = 0; i < NQ; ++i) lds(Qs + (NQ * ty + i) * LD + d, qv[i]);
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
+      for (int e = 0; e < 4; ++e) lds(Ks + (tx + 16 * e) * LD + d, kv[e]);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[i][e] = fmaf(qv[i], kv[e], s[i][e]);
+      for (int c = 0; c < 4; ++c)
+#pragma unroll
+        for (int i = 0; i < NQ; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[i][e] = fmaf(qv[i][c], kv[e][c], s[i][e]);
     }
     // every row of the tile sees every key of it?
-    const bool whole = !in_sink && k0 + BK - 1 <= q0 && (qlast - k0 < a.window) && k0 + BK <= kend;
+    const int k0 = lo + u0 - sinks;
+    const bool whole = u0 >= sinks && k0 + BK - 1 <= q0 && qlast - k0 < a.window && u0 + BK <= keys;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int row = q0 + 8 * ty + i;
+    for (int i = 0; i < NQ; ++i) {
+      const int row = q0 + NQ * ty + i;
       float mx = -INFINITY;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const int key = k0 + tx + 16 * e;
-        if (!whole && !(key < kend && key <= row && (row - key < a.window || key < a.sinks))) s[i][e] = -INFINITY;
+        const int u = u0 + tx + 16 * e, key = key_of(u);
+        if (!whole && !(u < keys && key <= row && (row - key < a.window || key < a.sinks))) s[i][e] = -INFINITY;
         mx = fmaxf(mx, s[i][e]);
       }
 #pragma unroll
@@ -127,7 +154,7 @@ __global__ void __launch_bounds__(128) window_simt_kernel(const WindowAttnArgs a
       for (int e = 0; e < 4; ++e) {
         const float p = exp2f(s[i][e] - ref);
         sum += p;
-        Ps[(tx + 16 * e) * LQ + 8 * ty + i] = p;
+        Ps[(NQ * ty + i) * LP + tx + 16 * e] = p;
       }
       l[i] = l[i] * corr + sum;  // this thread's keys; the sixteen threads of a row are added at the end
 #pragma unroll
@@ -135,32 +162,25 @@ __global__ void __launch_bounds__(128) window_simt_kernel(const WindowAttnArgs a
     }
     __syncwarp();  // a row's weights are written and read by the sixteen threads of one half warp
     auto add = [&](auto masked) {
-#pragma unroll 4
-      for (int k = 0; k < BK; ++k) {
-        const float4 pa = *reinterpret_cast<const float4*>(Ps + k * LQ + 8 * ty);
-        const float4 pb = *reinterpret_cast<const float4*>(Ps + k * LQ + 8 * ty + 4);
-        const float pv[8] = {pa.x, pa.y, pa.z, pa.w, pb.x, pb.y, pb.z, pb.w};
-        float vv[NC];
-        const float* vp = Vs + k * DH + NC * tx;
-        if constexpr (NC == 2) {
-          const float2 f = *reinterpret_cast<const float2*>(vp);
-          vv[0] = f.x, vv[1] = f.y;
-        } else {
+#pragma unroll 2
+      for (int k = 0; k < BK; k += 4) {
+        float pv[NQ][4];
 #pragma unroll
-          for (int c = 0; c < NC; c += 4) {
-            const float4 f = *reinterpret_cast<const float4*>(vp + c);
-            vv[c] = f.x, vv[c + 1] = f.y, vv[c + 2] = f.z, vv[c + 3] = f.w;
-          }
+        for (int i = 0; i < NQ; ++i) lds(Ps + (NQ * ty + i) * LP + k, pv[i]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          float vv[NC];
+          lds(Vs + (k + j) * LD + NC * tx, vv);
+#pragma unroll
+          for (int i = 0; i < NQ; ++i)
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+              if constexpr (decltype(masked)::value)
+                o[i][c] = pv[i][j] != 0.f ? fmaf(pv[i][j], vv[c], o[i][c]) : o[i][c];
+              else
+                o[i][c] = fmaf(pv[i][j], vv[c], o[i][c]);
+            }
         }
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-#pragma unroll
-          for (int c = 0; c < NC; ++c) {
-            if constexpr (decltype(masked)::value)
-              o[i][c] = pv[i] != 0.f ? fmaf(pv[i], vv[c], o[i][c]) : o[i][c];
-            else
-              o[i][c] = fmaf(pv[i], vv[c], o[i][c]);
-          }
       }
     };
     if (whole)
@@ -170,10 +190,10 @@ __global__ void __launch_bounds__(128) window_simt_kernel(const WindowAttnArgs a
   }
   T* out = static_cast<T*>(a.out) + static_cast<size_t>(g) * a.M * a.H * DH;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < NQ; ++i) {
 #pragma unroll
     for (int w = 8; w; w >>= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], w);
-    const int row = q0 + 8 * ty + i;
+    const int row = q0 + NQ * ty + i;
     if (row >= len) continue;
     const float inv = 1.f / l[i];  // a row sees itself: l > 0
     T* dst = out + (static_cast<size_t>(row) * a.H + h) * DH + NC * tx;
@@ -187,15 +207,27 @@ __global__ void __launch_bounds__(128) window_simt_kernel(const WindowAttnArgs a
   }
 }
 
-template <int DH, typename T>
-cudaError_t launch_simt(const WindowAttnArgs& a, cudaStream_t st) {
-  using S = WinSimt<DH>;
+template <int DH, typename T, int NQ>
+cudaError_t launch_rows(const WindowAttnArgs& a, cudaStream_t st) {
+  using S = WinSimt<DH, NQ>;
   static std::atomic<uint64_t> done;
-  cudaError_t e = allow_smem(reinterpret_cast<const void*>(window_simt_kernel<DH, T>), S::BYTES, done);
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(window_simt_kernel<DH, T, NQ>), S::BYTES, done);
   if (e != cudaSuccess) return e;
   const dim3 grid((a.M + S::BQ - 1) / S::BQ, a.H, a.G);
-  e = launch_pdl(window_simt_kernel<DH, T>, grid, dim3(128), S::BYTES, st, a);
+  e = launch_pdl(window_simt_kernel<DH, T, NQ>, grid, dim3(128), S::BYTES, st, a);
   return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+template <int DH, typename T>
+cudaError_t launch_simt(const WindowAttnArgs& a, cudaStream_t st) {
+  // 16 rows a CTA where all those CTAs run at once. fp32, window 256, 16 sinks, of 16 rows and of 32: two
+  // sequences of 1040 with 4 heads of 64 (520 CTAs of 16 rows, four an SM) 37 and 43 us, with 8 heads 68 and 48;
+  // bf16 heads of 32 (eight an SM), 8 of them 37 and 38, 32 and four sequences 239 and 192. (64 rows a
+  // CTA: 57, 76, 50 and 221.)
+  using S = WinSimt<DH, 2>;
+  constexpr int at_once = 148 * (227 * 1024 / (S::BYTES + 1024));
+  const long long ctas = static_cast<long long>((a.M + S::BQ - 1) / S::BQ) * a.H * a.G;
+  return ctas <= at_once ? launch_rows<DH, T, 2>(a, st) : launch_rows<DH, T, 4>(a, st);
 }
 
 }  // namespace

@@ -430,7 +430,8 @@ WINDOW = [  # dh, H, Hkv, G, M, lens, window, sinks
     (64, 8, 1, 2, 700, [700, 33], 33, 300), (128, 4, 1, 1, 333, None, 200, 16), (128, 3, 1, 2, 257, [200, 257], 0, 0),
     (128, 2, 2, 1, 513, None, 128, 128), (32, 4, 2, 2, 150, [1, 150], 40, 3), (64, 20, 1, 1, 100, None, 30, 9),
     (64, 40, 2, 1, 65, None, 0, 5), (64, 16, 1, 1, 400, None, 256, 0), (128, 8, 1, 1, 384, [383], 383, 1),
-    (64, 5, 1, 2, 290, None, 131, 8), (64, 2, 1, 1, 1100, None, 1040, 3), (128, 12, 4, 1, 200, None, 1000, 1000)]
+    (64, 5, 1, 2, 290, None, 131, 8), (64, 2, 1, 1, 1100, None, 1040, 3), (128, 12, 4, 1, 200, None, 1000, 1000),
+    (64, 32, 8, 3, 333, [333, 0, 67], 90, 70), (128, 16, 2, 2, 300, [300, 17], 129, 5), (32, 24, 6, 3, 333, None, 77, 33)]
 
 
 @gpu
