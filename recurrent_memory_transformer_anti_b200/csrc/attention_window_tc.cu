@@ -21,7 +21,7 @@
 //                (P has TMEM columns of its own); at 128, where P overwrites S and the next S follows
 //                P V in the pipe, one thread issues for both in turn (two threads mix their
 //                MMAs, which doubles each product's latency: 139 us for six prompts of up to 2063 rows,
-//                window 777, against 111);
+//                window 777, against 111; 106 since, with no wait for P V: S behind it in the pipe says so);
 //   up to 3      look through every V tile that some row sees only in part, before its P V: rows
 //                behind the sequence's end, and rows that hold a value that is not finite, are
 //                zeroed (0 * inf would reach rows that do not see them); the latter are noted
@@ -40,7 +40,8 @@
 // of each softmax warp's own chain (barriers, TMEM accesses, one dependent instruction after
 // another), which four such warps per scheduler hide only in part, since they run in step. Measured and not better: one
 // thread a row with 168 or 200 registers (4,840), four query tiles against 64-key tiles (4,750), one issuing
-// thread that takes whatever is ready (4,800), longer waits between polls, a head start for A.
+// thread that takes whatever is ready (4,800), three buffers of S in turn with P in their columns, so that
+// S is always there before its softmax (4,850), longer waits between polls, a head start for A.
 // 65,536 tokens, 32/8 heads of 64, window 1024, 4 sinks: 1.20 ms, 455 TFLOP/s.
 #include <cuda.h>
 
@@ -76,7 +77,7 @@ struct WtCfg {
   static constexpr int SLOT_OFF = MX_OFF + 2 * 2 * 128 * 4;
   static constexpr int SMEM = 1024 + SLOT_OFF + 16;
   static constexpr int S_COL = 0, O_COL = 256, P_COL = OVERLAY ? 0 : 256 + 2 * HD;
-  static constexpr int P_STEP = OVERLAY ? 128 : 64;
+  static constexpr int P_STEP = OVERLAY ? 128 : 64, P_HALF = OVERLAY ? 64 : 32;  // each half where its own S was
 };
 
 struct WtArgs {
@@ -424,8 +425,8 @@ __global__ void __launch_bounds__(640, 1)
               const uint64_t bd = dv + static_cast<uint32_t>(pst * (C::TILE >> 4));
 #pragma unroll
               for (int k = 0; k < 128 / 16; ++k)  // P from TMEM: 16 keys per step = 8 columns of pairs
-                sm100::mma_f16_tmem_a(tmem + C::O_COL + HD * x, tmem + C::P_COL + C::P_STEP * x + 8 * k,
-                                      bd + static_cast<uint32_t>(k * 2048 >> 4), idO, !fresh_o[i] || k > 0);
+                sm100::mma_f16_tmem_a(tmem + C::O_COL + HD * x,
+                                      tmem + C::P_COL + C::P_STEP * x + C::P_HALF * (k >> 2) + 8 * (k & 3), bd + static_cast<uint32_t>(k * 2048 >> 4), idO, !fresh_o[i] || k > 0);
               sm100::mma_commit(bar(C::OREADY + x));
               sm100::mma_commit(bar(C::VEMPTY + pst));
               if (fresh_o[i]) ++no[i];
@@ -504,7 +505,7 @@ __global__ void __launch_bounds__(640, 1)
     const uint32_t loff = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t tS = tmem + loff + C::S_COL + 128 * x + 64 * half;
     const uint32_t tO = tmem + loff + C::O_COL + HD * x + HD / 2 * half;
-    const uint32_t tP = tmem + loff + C::P_COL + C::P_STEP * x + 32 * half;
+    const uint32_t tP = tmem + loff + C::P_COL + C::P_STEP * x + C::P_HALF * half;
     float* const mx_own = reinterpret_cast<float*>(smem + C::MX_OFF) + (2 * x + half) * 128 + r;
     const float* const mx_other = reinterpret_cast<float*>(smem + C::MX_OFF) + (2 * x + 1 - half) * 128 + r;
     const int pair = 1 + 4 * x + quarter;  // named barrier of the two warps of these rows
@@ -559,7 +560,7 @@ __global__ void __launch_bounds__(640, 1)
         await(C::SFULL + x, n);
         if (idle) {  // the same waits and arrivals as the busy warps, in the same order
           if (!C::OVERLAY) sm100::mbar_arrive(bar(C::SFREE + x));
-          if (n > 0) await(C::OREADY + x, n - 1);
+          if (!C::OVERLAY && n > 0) await(C::OREADY + x, n - 1);
           sm100::mbar_arrive(bar(C::PREADY + x));
           first = false;
           ++n;
@@ -585,11 +586,10 @@ __global__ void __launch_bounds__(640, 1)
           }
         };
         float corr = 1.f, sum;
-        bool rescale = false, over = first, redone = first;
+        bool rescale = false, over = first;
         uint32_t pk[32];
         for (int tries = first ? 1 : 0;; ++tries) {
           if (tries > 0) {
-            redone = true;
             // the row maximum, over both halves
             float mxp[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll 1
@@ -650,22 +650,21 @@ __global__ void __launch_bounds__(640, 1)
         }
         sm100::tc_fence_before();
         if (!C::OVERLAY) sm100::mbar_arrive(bar(C::SFREE + x));
-        if (C::OVERLAY && redone) meet();  // P goes where the other half's S was (else they met above)
-        if (n > 0) {
-          // P V of the tile before must be done before P and O change
+        // P V of the tile before must be done before P and O change; in S's columns that is so, S came after it
+        if (!C::OVERLAY && n > 0) {
           await(C::OREADY + x, n - 1);
           sm100::tc_fence_after();
-          if (__any_sync(0xffffffffu, rescale)) {
-            const float f = rescale ? corr : 1.f;
+        }
+        if (__any_sync(0xffffffffu, rescale)) {
+          const float f = rescale ? corr : 1.f;
 #pragma unroll 1
-            for (int oc = 0; oc < HD / 32; ++oc) {
-              uint32_t o[16];
-              sm100::tmem_ld16(tO + 16 * oc, o);
-              sm100::tmem_wait_ld();
+          for (int oc = 0; oc < HD / 32; ++oc) {
+            uint32_t o[16];
+            sm100::tmem_ld16(tO + 16 * oc, o);
+            sm100::tmem_wait_ld();
 #pragma unroll
-              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(u2f(o[i]) * f);
-              sm100::tmem_st16(tO + 16 * oc, o);
-            }
+            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(u2f(o[i]) * f);
+            sm100::tmem_st16(tO + 16 * oc, o);
           }
         }
         sm100::tmem_st16(tP, pk);  // keys 2c, 2c + 1 in column c
