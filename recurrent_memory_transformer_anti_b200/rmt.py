@@ -159,7 +159,9 @@ def _ptr(x):
 
 def _ptr32(x):
     """Raw address of an int32 array (None -> NULL)."""
-    if x is not None and not isinstance(x, int) and "int32" not in str(x.dtype):
+    if x is None or isinstance(x, int):
+        return x
+    if "int32" not in str(x.dtype):
         raise TypeError(f"an int32 array is needed, not {x.dtype}")
     return _ptr(x)
 
@@ -167,23 +169,28 @@ def _ptr32(x):
 def _rows(x, n: int, M: int, width: int, dtype: str):
     """Address and row stride (elements) of n * M rows of `width` values: a tensor [n, M, ...] whose rows
     are contiguous and equally spaced, possibly a slice of wider rows."""
-    if _ROW_TYPES.get(str(x.dtype)) != dtype:
+    if _row_types.get(x.dtype) != dtype and _ROW_TYPES.get(str(x.dtype)) != dtype:
         raise TypeError(f"rows of type {x.dtype} given as {dtype!r}")
+    _row_types[x.dtype] = dtype  # a lookup by name the first time only
     shape, st = x.shape, x.stride()
     if len(shape) < 3 or shape[0] != n or shape[1] != M or x.numel() != n * M * width:
         raise ValueError(f"rows must be [{n}, {M}, {width}], not {tuple(shape)}")
     ld = st[1] if M > 1 else st[0] if n > 1 else width
     ok = ld >= width and (n == 1 or st[0] == M * ld)
-    step = 1
-    for d in range(len(shape) - 1, 1, -1):
-        ok = ok and (shape[d] == 1 or st[d] == step)
-        step *= shape[d]
+    if len(shape) == 3:
+        ok = ok and (width == 1 or st[2] == 1)
+    else:
+        step = 1
+        for d in range(len(shape) - 1, 1, -1):
+            ok = ok and (shape[d] == 1 or st[d] == step)
+            step *= shape[d]
     if not ok:
         raise ValueError("rows must be contiguous and equally spaced")
     return x.data_ptr(), ld
 
 
 _ROW_TYPES = {"torch.bfloat16": "bf16", "torch.float32": "f32"}
+_row_types = {}  # dtype -> its name above, as far as seen
 
 
 _current_stream = None  # () -> the raw current stream, once CUDA was found available
