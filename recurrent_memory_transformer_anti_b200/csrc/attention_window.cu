@@ -6,11 +6,11 @@
 // to the last row's own, numbered u = 0, 1, .. without a gap. Each thread keeps NQ queries x 4 keys of the
 // scores and NQ queries x dh/16 channels of the output in registers; a row's maximum and sum run along
 // (one pass over the keys).
-// Key rows past the sequence's end are never read. A weight of zero adds nothing even when the
-// value it belongs to is not finite, so what is masked cannot reach a row.
+// Key rows past the sequence's end are never read. A masked key's weight is zero, and zero adds nothing even
+// when the value it belongs to is not finite; a weight that is too small for fp32 is its smallest number.
 // Bound by the fp32 FMA pipe and the shared-memory reads that feed it: 16 bytes at a time, 8 of them for
-// 64 FMA. Two sequences of 1040 rows, 32 / 8 heads of 64, window 256, 16 sinks: 161 us, 25 TFLOP/s of
-// what is visible; two of 208 rows with 4 / 2 heads, window 64, which only fill the SMs with 16 rows a CTA: 8.6 us.
+// 64 FMA. Two sequences of 1040 rows, 32 / 8 heads of 64, window 256, 16 sinks: 166 us, 24 TFLOP/s of
+// what is visible; two of 208 rows with 4 / 2 heads, window 64, too few to fill the SMs: 9.0 us.
 // Serves fp32, and bf16 heads of 32 (bf16 heads of 64 and 128: attention_window_tc.cu).
 #include "cache4.cuh"
 #include "launch.h"
@@ -137,10 +137,12 @@ __global__ void __launch_bounds__(128) window_simt_kernel(const WindowAttnArgs a
     for (int i = 0; i < NQ; ++i) {
       const int row = q0 + NQ * ty + i;
       float mx = -INFINITY;
+      bool seen[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int u = u0 + tx + 16 * e, key = key_of(u);
-        if (!whole && !(u < keys && key <= row && (row - key < a.window || key < a.sinks))) s[i][e] = -INFINITY;
+        seen[e] = whole || (u < keys && key <= row && (row - key < a.window || key < a.sinks));
+        if (!seen[e]) s[i][e] = -INFINITY;
         mx = fmaxf(mx, s[i][e]);
       }
 #pragma unroll
@@ -152,7 +154,8 @@ __global__ void __launch_bounds__(128) window_simt_kernel(const WindowAttnArgs a
       float sum = 0.f;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const float p = exp2f(s[i][e] - ref);
+        float p = exp2f(s[i][e] - ref);
+        if (!whole && seen[e] && p == 0.f) p = 1.4e-45f;  // not 0, which stands for a masked key below
         sum += p;
         Ps[(NQ * ty + i) * LP + tx + 16 * e] = p;
       }

@@ -157,12 +157,25 @@ def _ptr(x):
     raise TypeError(f"cannot take the address of {type(x)}")
 
 
-def _ptr32(x):
-    """Raw address of an int32 array (None -> NULL)."""
+def _ptr32(x, count=None):
+    """Raw address of an int32 array (None -> NULL), of at least `count` entries if given."""
     if x is None or isinstance(x, int):
         return x
     if "int32" not in str(x.dtype):
         raise TypeError(f"an int32 array is needed, not {x.dtype}")
+    if count is not None and x.shape[0] < count:
+        raise ValueError(f"{count} entries are needed, not {tuple(x.shape)}")
+    return _ptr(x)
+
+
+def _whole(x, count: int, dtype: str):
+    """Address of a contiguous tensor of at least `count` values (an address is taken as it is)."""
+    if x is None or isinstance(x, int):
+        return x
+    if _row_types.get(x.dtype) != dtype and _ROW_TYPES.get(str(x.dtype)) != dtype:
+        raise TypeError(f"a tensor of type {x.dtype} given as {dtype!r}")
+    if x.numel() < count:
+        raise ValueError(f"{count} values are needed, not {tuple(x.shape)}")
     return _ptr(x)
 
 
@@ -391,8 +404,9 @@ def rmt_rmsnorm(x, g, y, rows, d, eps, dtype="f32", stream=None) -> None:
 
 def rmt_attention_window(qkv, out, G, M, H, Hkv, dh, window, sinks=0, lens=None, dtype="bf16", stream=None) -> None:
     """Attention over a sliding window (0: none) and the first `sinks` tokens; lens: int32 [G] on the device or None."""
-    _check(_lib.rmt_attention_window(_ptr(qkv), _ptr(out), G, M, H, Hkv, dh, window, sinks, _ptr32(lens),
-                                     DTYPES[dtype], _stream(stream)), "rmt_attention_window")
+    _check(_lib.rmt_attention_window(_whole(qkv, G * M * (H + 2 * Hkv) * dh, dtype), _whole(out, G * M * H * dh, dtype),
+                                     G, M, H, Hkv, dh, window, sinks, _ptr32(lens, G), DTYPES[dtype],
+                                     _stream(stream)), "rmt_attention_window")
 
 
 class Cache:
@@ -430,7 +444,7 @@ def _cache_rows(fn, name, cache, k, v, M, n_new, dtype, stream):
     pv, ldv = _rows(v, cache.n_seqs, M, cache.width, dtype)
     if ld != ldv:
         raise ValueError("k and v need the same row stride")
-    _check(fn(cache.ref, pk, pv, ld, M, _ptr32(n_new), DTYPES[dtype], _stream(stream)), name)
+    _check(fn(cache.ref, pk, pv, ld, M, _ptr32(n_new, cache.n_seqs), DTYPES[dtype], _stream(stream)), name)
 
 
 def rmt_cache_write(cache: Cache, k, v, M, n_new=None, dtype="bf16", stream=None) -> None:
@@ -454,7 +468,8 @@ def rmt_attention_cache(cache: Cache, q, out, n_q, H, window, sinks, workspace, 
     """Attention of the newest n_q tokens of each sequence (q rows [n_seqs, n_q, H * head_dim], a view into
     wider rows allowed) over the cache. workspace: a uint8 tensor of rmt_attention_cache_workspace bytes."""
     pq, ldq = _rows(q, cache.n_seqs, n_q, H * cache.head_dim, dtype)
-    _check(_lib.rmt_attention_cache(cache.ref, pq, ldq, _ptr(out), n_q, H, window, sinks,
+    _check(_lib.rmt_attention_cache(cache.ref, pq, ldq, _whole(out, cache.n_seqs * n_q * H * cache.head_dim, dtype),
+                                    n_q, H, window, sinks,
                                     _ptr(workspace), workspace.numel() * workspace.element_size(), DTYPES[dtype],
                                     _stream(stream)), "rmt_attention_cache")
 

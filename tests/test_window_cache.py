@@ -483,6 +483,25 @@ def test_window_attention_keeps_masked_values_out(cuda_ok, dtype, bad, dh):
 
 
 @gpu
+@pytest.mark.parametrize("dtype,dh", [("bf16", 32), ("f32", 64), ("bf16", 64), ("bf16", 128), ("f32", 128)])
+def test_window_attention_shows_a_value_that_is_not_finite_whatever_its_weight(cuda_ok, dtype, dh):
+    """Token 7's weight is below 2^-1000 in every row but its own; its value is infinite."""
+    H, M, window, sinks = 2, 150, 60, 2
+    qkv = torch.zeros(1, M, 3 * H * dh, dtype=TORCH[dtype], device="cuda")
+    qkv[..., :2 * H * dh] = 16.0
+    qkv[0, 7, H * dh:2 * H * dh] = -16.0  # scores 256 sqrt(dh) and its negative, powers of e
+    qkv[..., 2 * H * dh:] = normal(3, (1, M, H * dh), dtype)
+    qkv[0, 7, 2 * H * dh + 3] = float("inf")  # head 0
+    out = torch.zeros(1, M, H * dh, dtype=TORCH[dtype], device="cuda")
+    rmt.rmt_attention_window(qkv, out, 1, M, H, H, dh, window, sinks, dtype=dtype)
+    rmt.rmt_sync(None)
+    fin = torch.isfinite(out.reshape(M, H, dh)).all(-1).cpu().numpy()
+    sees = visible(np.arange(M), np.array([7]), window, sinks)[:, 0]
+    np.testing.assert_array_equal(fin[:, 0], ~sees)
+    assert fin[:, 1].all()
+
+
+@gpu
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_window_attention_of_large_and_small_queries(cuda_ok, dtype):
     H, Hkv, dh, M = 7, 1, 64, 300
@@ -712,3 +731,14 @@ def test_page_bytes_and_binding_checks():
                               (x[:, :4, :64], 64, "bf16"), (x[..., :64].transpose(0, 1), 64, "bf16")):
         with pytest.raises((ValueError, TypeError)):
             rmt._rows(bad, 2, 5, width, dtype)
+    w, o = torch.zeros(2, 5, 96, dtype=torch.bfloat16), torch.zeros(2, 5, 32, dtype=torch.bfloat16)
+    for args, kw in (((w, o[:, :4].clone()), {}), ((w.float(), o), {}), ((w, o.float()), {}), ((w, w[..., :32]), {}),
+                     ((w[..., :64].clone(), o), {}), ((w, o), dict(lens=z[:1])), ((w, o), dict(lens=z.long()))):
+        with pytest.raises((ValueError, TypeError)):  # out or qkv too short, of the wrong type or not contiguous; lens
+            rmt.rmt_attention_window(*args, 2, 5, 1, 1, 32, 0, **kw)
+    k = torch.zeros(2, 5, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        rmt.rmt_cache_write(c, k, k, 5, n_new=z[:1])
+    for out in (k[:, :4].clone(), k.float(), k[..., :32]):
+        with pytest.raises((ValueError, TypeError)):
+            rmt.rmt_attention_cache(c, k, out, 5, 1, 0, 0, torch.zeros(1 << 20, dtype=torch.uint8))
