@@ -1,10 +1,10 @@
 // Attention of a sequence's newest tokens over its pages of the 4-bit key/value cache.
 //
-// One pass over the codes, which is what bounds it: 72 dh bytes per 64 tokens and kv head. A unit of
+// One pass over the codes: 72 dh bytes per 64 tokens and kv head. A unit of
 // work is 64 tokens of one kv head (32 at head_dim 128: 4608 bytes either way) for one tile of query
 // rows; an item is what one (sequence, kv head, row tile) sees of the cache, without what lies between
 // the sinks and the window. Two ways of dealing the units, by the most units an item can have:
-//   up to kWholeUnits: a team of warps takes whole items, each warp every so-manieth unit, and adds
+//   short items (deal_whole): a team of warps takes whole items, each warp every so-manieth unit, and adds
 //     their results in shared memory: one launch, nothing read before the item's own length. A
 //     team has as many warps of a CTA as leave every item a team at once, at most one per unit.
 //   more: the units of all items form one list (lengths are read on the device), and each warp
@@ -38,8 +38,6 @@ using cache4::CacheArgs;
 using cache4::kPage;
 
 constexpr int kMaxWarps = 148 * 16;  // that share a list of units: 16 per SM
-constexpr int kLeastUnits = 4;   // of a warp's stretch
-constexpr int kWholeUnits = 32;  // items up to this many units are not split
 constexpr float kCodeScale = 128.f;  // operands hold 2^-7 of a value
 constexpr uint32_t kWideScale = 224;  // scale bytes from here on take the exact way (dequant)
 
@@ -87,7 +85,7 @@ struct Deal {
   int warps, units, each, more;
   __device__ __forceinline__ Deal(int units_, int grid_warps) {
     units = units_;
-    warps = max(1, min(grid_warps, (units + kLeastUnits - 1) / kLeastUnits));
+    warps = max(1, min(grid_warps, units));
     each = units / warps;
     more = units - each * warps;
   }
@@ -192,18 +190,21 @@ struct Item {
   Span s;
 };
 
-// Warps of a CTA, one CTA per SM: 16 of at most 128 registers, but where two row tiles of 128
-// channels need more: 12 of 168. (Of two CTAs with 8 warps each the first on an SM is served first:
-// it ended after 38 us of 64 sequences' 50, the other's four warps per scheduler then ran alone.)
-template <int DH, int NT>
+// Warps of a CTA, one CTA per SM: 16 of at most 128 registers, but fewer with more where they would spill too
+// much. 64 sequences of 8192 tokens, bf16: two row tiles of 128 channels (16 heads to one) 8 warps 41 us, 12
+// 48; two of 64 channels (32 heads to two, 16,384 tokens) 12 warps 66, 16 75; fp32 of 128 channels
+// (32 / 8 heads) 12 warps 185, 16 197; one tile of bf16 of 128 channels 16 warps 148, 12 154. (Of
+// two CTAs with 8 warps each the first on an SM is served first: it ended after 38 us of 64 sequences'
+// 50, the other's four warps per scheduler then ran alone.)
+template <int DH, typename T, int NT>
 struct Shape {
-  static constexpr bool WIDE = DH == 128 && NT == 2;
-  static constexpr int WARPS = WIDE ? 12 : 16;
+  static constexpr bool F32 = std::is_same_v<T, float>;
+  static constexpr int WARPS = DH == 128 && NT == 2 ? 8 : (DH == 64 && NT == 2) || (DH == 128 && F32) ? 12 : 16;
 };
 
-template <int DH, int NT, bool WHOLE>
+template <int DH, typename T, int NT, bool WHOLE>
 struct DecodeSmem {
-  static constexpr int kWarps = Shape<DH, NT>::WARPS;
+  static constexpr int kWarps = Shape<DH, T, NT>::WARPS;
   static constexpr int STAGES = WHOLE ? 2 : 3;  // of a warp's ring
   static constexpr int RING = 0;
   static constexpr int LD = DH + 4;
@@ -217,9 +218,9 @@ struct DecodeSmem {
 };
 
 template <int DH, typename T, int NT, bool WHOLE>
-__global__ void __launch_bounds__(32 * Shape<DH, NT>::WARPS, 1) cache_attn_kernel(const DecodeArgs a) {
+__global__ void __launch_bounds__(32 * Shape<DH, T, NT>::WARPS, 1) cache_attn_kernel(const DecodeArgs a) {
   using U = Unit<DH>;
-  using S = DecodeSmem<DH, NT, WHOLE>;
+  using S = DecodeSmem<DH, T, NT, WHOLE>;
   constexpr int kStages = S::STAGES, kWarps = S::kWarps, kThreads = 32 * kWarps;
   constexpr bool SPLIT = std::is_same_v<T, float>;  // two f16 terms per query and weight
   constexpr int TERMS = SPLIT ? 2 : 1;
@@ -844,6 +845,15 @@ long long most_units(int max_pages, int n_q, int dh, int window, int sinks) {
   const long long seen = (static_cast<long long>(window) + n_q + tok - 2) / tok + 1 + (sinks + tok - 1LL) / tok;
   return all < seen ? all : seen;
 }
+// Whether items are dealt whole. Whole, an item takes its warps' share of the longest one's units; dealt in
+// stretches, the average, and a second kernel. bf16, 32 / 8 heads of 64, all lengths alike, whole and in
+// stretches, for 2048, 4096 and 8192 tokens (32, 64 and 128 units): one sequence (8 items) 9.4 and 9.8, 14.3 and
+// 10.0, 23.8 and 11.1 us; 8 sequences 9.8 and 12.5, 14.8 and 16.8, 24.2 and 21.3; 16 sequences 10.5 and 16.4,
+// 15.4 and 21.3, 25.3 and 30.5; 64 sequences 24.8 and 30.1, 44.9 and 49.6, 82.1 and 82.3. Where lengths differ
+// the shares of whole items do too, so beyond 32 units only items that have a CTA each and would fill most SMs.
+bool deal_whole(long long most, long long items) {
+  return most <= 32 || (most <= 64 && items >= 64 && items <= 148);
+}
 struct Plan {
   bool whole;
   long long items, units;
@@ -856,11 +866,14 @@ Plan plan_of(int n_seqs, int max_pages, int n_q, int tiles, int Hkv, int dh, int
   const long long most = most_units(max_pages, n_q, dh, window, sinks);
   p.items = static_cast<long long>(n_seqs) * Hkv * tiles;
   p.units = p.items * most;
-  p.whole = most <= kWholeUnits;
-  // the widest team that leaves every item one at once (148 SMs)
+  p.whole = deal_whole(most, p.items);
+  // the widest team that leaves every item one at once (148 SMs; 64 sequences of 1024 tokens, 512 items: teams
+  // of 4 15.0 us, of 16 25.0; 32 sequences: 10.0 and 13.3)
   p.team = cta_warps;
   while (p.team > 1 && (cta_warps % p.team || p.team > most || p.items * p.team > 148LL * cta_warps)) --p.team;
-  const long long share = p.whole ? cta_warps / p.team : cta_warps * kLeastUnits;
+  // a short list over all SMs, one unit a warp (one sequence of 4096 tokens 10.0 us, 11.9 with 16 warps a CTA at
+  // work, 18.4 with stretches of at least four units)
+  const long long share = p.whole ? cta_warps / p.team : 1;
   const long long want = ((p.whole ? p.items : p.units) + share - 1) / share;
   p.ctas = static_cast<int>(want < 148 ? want : 148);  // one per SM
   p.warps = p.ctas * cta_warps;
@@ -869,7 +882,7 @@ Plan plan_of(int n_seqs, int max_pages, int n_q, int tiles, int Hkv, int dh, int
 
 template <int DH, typename T, int NT>
 cudaError_t launch_decode(const CacheAttnArgs& c, cudaStream_t st) {
-  constexpr int kWarps = Shape<DH, NT>::WARPS;
+  constexpr int kWarps = Shape<DH, T, NT>::WARPS;
   DecodeArgs a{};
   a.c = c.c;
   a.span = {c.c.max_pages * kPage, c.n_q, c.window, c.sinks};
@@ -879,7 +892,7 @@ cudaError_t launch_decode(const CacheAttnArgs& c, cudaStream_t st) {
   a.tiles = (a.rows + 8 * NT - 1) / (8 * NT);
   const Plan p = plan_of(c.c.n_seqs, c.c.max_pages, c.n_q, a.tiles, c.c.Hkv, DH, c.window, c.sinks, kWarps);
   auto kernel = p.whole ? cache_attn_kernel<DH, T, NT, true> : cache_attn_kernel<DH, T, NT, false>;
-  const int smem = p.whole ? DecodeSmem<DH, NT, true>::BYTES : DecodeSmem<DH, NT, false>::BYTES;
+  const int smem = p.whole ? DecodeSmem<DH, T, NT, true>::BYTES : DecodeSmem<DH, T, NT, false>::BYTES;
   static std::atomic<uint64_t> done[2];
   cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), smem, done[p.whole]);
   if (e != cudaSuccess) return e;
@@ -893,7 +906,8 @@ cudaError_t launch_decode(const CacheAttnArgs& c, cudaStream_t st) {
     // threads for a group of about four parts each of an item's parts (were they alike): its rows
     // together, or fewer rows a CTA where that takes more than 1024
     const int rows = 8 * NT < a.rows ? 8 * NT : a.rows;
-    const int want = static_cast<int>((p.warps + 4 * p.items - 1) / (4 * p.items));
+    const long long parts = p.units < p.warps ? p.units : p.warps;
+    const int want = static_cast<int>((parts + 4 * p.items - 1) / (4 * p.items));
     int per = rows;
     while (per > 1 && per * (DH / 4) * want > 1024) per = (per + 1) / 2;
     const int threads = per * (DH / 4) * want < 1024 ? (per * (DH / 4) * want + 31) / 32 * 32 : 1024;
