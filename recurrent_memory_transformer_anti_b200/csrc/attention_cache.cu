@@ -14,6 +14,11 @@
 //     order of the keys: no atomics, equal bits.
 // Each warp has its own ring of bulk copies.
 //
+// Bound by instructions, not by HBM: 64 sequences of 1 to 8192 tokens (166 MB; 32 / 8 heads of 64, bf16) take
+// 51 us and 5 for the second kernel, 3.0 TB/s, with the schedulers issuing in 54% of all cycles, the integer
+// pipe at 49%, the tensor pipe at 21% and HBM at 41%; one of 131,072 tokens 33 us in all, of which 3 go to
+// the chain of length, page number and codes before the first product.
+//
 // Arithmetic. Query rows are the MMA's N (8 or 16 rows: the heads of a group, times the tokens),
 // keys or channels its M, so that few rows waste nothing: S^T = K Q^T, O^T = V^T P^T
 // (mma.sync m16n8k16, f16 operands, fp32 sums: the codes turn into operands in registers, and tcgen05
