@@ -186,13 +186,15 @@ def _rows(x, n: int, M: int, width: int, dtype: str):
         raise TypeError(f"rows of type {x.dtype} given as {dtype!r}")
     _row_types[x.dtype] = dtype  # a lookup by name the first time only
     shape, st = x.shape, x.stride()
-    if len(shape) < 3 or shape[0] != n or shape[1] != M or x.numel() != n * M * width:
+    if len(shape) < 3 or shape[0] != n or shape[1] != M:
         raise ValueError(f"rows must be [{n}, {M}, {width}], not {tuple(shape)}")
     ld = st[1] if M > 1 else st[0] if n > 1 else width
     ok = ld >= width and (n == 1 or st[0] == M * ld)
-    if len(shape) == 3:
-        ok = ok and (width == 1 or st[2] == 1)
+    if len(shape) == 3 and shape[2] == width:
+        ok = ok and (st[2] == 1 or width == 1)
     else:
+        if x.numel() != n * M * width:
+            raise ValueError(f"rows must be [{n}, {M}, {width}], not {tuple(shape)}")
         step = 1
         for d in range(len(shape) - 1, 1, -1):
             ok = ok and (shape[d] == 1 or st[d] == step)
@@ -441,9 +443,12 @@ def rmt_cache(pages, page_table, lens, n_kv_heads: int, head_dim: int) -> Cache:
 
 def _cache_rows(fn, name, cache, k, v, M, n_new, dtype, stream):
     pk, ld = _rows(k, cache.n_seqs, M, cache.width, dtype)
-    pv, ldv = _rows(v, cache.n_seqs, M, cache.width, dtype)
-    if ld != ldv:
-        raise ValueError("k and v need the same row stride")
+    if v.dtype is k.dtype and v.shape == k.shape and v.stride() == k.stride():
+        pv = v.data_ptr()
+    else:
+        pv, ldv = _rows(v, cache.n_seqs, M, cache.width, dtype)
+        if ld != ldv:
+            raise ValueError("k and v need the same row stride")
     _check(fn(cache.ref, pk, pv, ld, M, _ptr32(n_new, cache.n_seqs), DTYPES[dtype], _stream(stream)), name)
 
 

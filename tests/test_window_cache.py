@@ -728,7 +728,8 @@ def test_page_bytes_and_binding_checks():
     assert rmt._rows(x[:, :1, :64], 2, 1, 64, "bf16")[1] == 500
     assert rmt._rows(torch.zeros(1, 1, 2, 32), 1, 1, 64, "f32")[1] == 64
     for bad, width, dtype in ((x[:, ::2, :64], 64, "bf16"), (x[..., :128:2], 50, "bf16"), (x[..., :64], 64, "f32"),
-                              (x[:, :4, :64], 64, "bf16"), (x[..., :64].transpose(0, 1), 64, "bf16")):
+                              (x[:, :4, :64], 64, "bf16"), (x[..., :64].transpose(0, 1), 64, "bf16"),
+                              (x[..., 0], 1, "bf16"), (x[0, 0], 100, "bf16"), (x, 64, "bf16")):
         with pytest.raises((ValueError, TypeError)):
             rmt._rows(bad, 2, 5, width, dtype)
     w, o = torch.zeros(2, 5, 96, dtype=torch.bfloat16), torch.zeros(2, 5, 32, dtype=torch.bfloat16)
