@@ -28,21 +28,26 @@
 //                in a bit mask, and the rows that do see one give NaN;
 //   warps 4-11   softmax of A, 12-19 of B: two threads a row, 64 columns each.
 // A row's reference (what its scores are taken relative to) is the maximum of the first tile it sees;
-// later tiles take their exponentials against it in one pass, and only a tile whose weights add
-// up to more than 2^12 is gone through again for its maximum, with O rescaled: no weight passes 2^12 (they
-// are held as bf16, whose relative precision is the same everywhere; an operand pair has one type).
+// later tiles take their exponentials against it in one pass. Weights are held as bf16, whose relative
+// precision is the same everywhere (an operand pair has one type), and summed in fp32, so a reference
+// that turns out too low does no harm until a weight or an output leaves fp32's range. At head_dim 64 nothing is
+// checked on the way: an item with a row whose weights add up to more than 2^60 (or, from 2^12 on, whose O is not
+// finite) is noted, and after all items the CTA goes through the noted ones again, carefully: a tile whose
+// weights add up to more than 2^12 is gone through again for its maximum, with O rescaled. At 128 that is
+// done at once. (The careful way has both threads of a row meet at every tile, and a loop where the other has
+// straight code: 1.20 ms instead of 1.01 for the long prompt below; at 128 102 us and 104.)
 // Every wait is bounded; a timeout drains in-flight copies and MMAs, frees TMEM and sets the
 // error word.
 //
 // Bound: the 32,768 exponentials of two 128 x 128 tiles take the special function unit 2048 cycles
-// (the MMAs 1024, or 2048 at head_dim 128); the step takes 4,500 at head_dim 64. With one
-// query tile in flight it takes 3,200, with the exponentials left out 3,700: what is left is the latency
-// of each softmax warp's own chain (barriers, TMEM accesses, one dependent instruction after
-// another), which four such warps per scheduler hide only in part, since they run in step. Measured and not better: one
+// (the MMAs 1024, or 2048 at head_dim 128); the step takes 3,800 at head_dim 64: the instructions of the
+// softmax warps and the latency of each one's own chain (barriers, TMEM accesses, one dependent
+// instruction after another), which four such warps per scheduler hide only in part. A tile that some row sees
+// in part costs about 1.4 times one that all see. Measured when the step took 4,500, and not better: one
 // thread a row with 168 or 200 registers (4,840), four query tiles against 64-key tiles (4,750), one issuing
 // thread that takes whatever is ready (4,800), three buffers of S in turn with P in their columns, so that
 // S is always there before its softmax (4,850), longer waits between polls, a head start for A.
-// 65,536 tokens, 32/8 heads of 64, window 1024, 4 sinks: 1.20 ms, 455 TFLOP/s.
+// 65,536 tokens, 32/8 heads of 64, window 1024, 4 sinks: 1.01 ms, 540 TFLOP/s.
 #include <cuda.h>
 
 #include "cache4.cuh"
@@ -54,12 +59,15 @@ namespace {
 
 using bf16 = __nv_bfloat16;
 
+constexpr int kLostWords = 64;
+
 template <int HD>
 struct WtCfg {
   static constexpr int SUB = 128 * 64 * 2;  // one 128-row x 64-column swizzled block
   static constexpr int NSUB = HD / 64;
   static constexpr int TILE = NSUB * SUB;
   static constexpr bool OVERLAY = HD == 128;  // P in S's columns (512 TMEM columns hold no more)
+  static constexpr bool TWICE = HD == 64;  // items in a first pass without, a second with raised references
   static constexpr int NX = OVERLAY ? 2 : 1;       // query tiles of an issuing thread (warps 1 .. 2 / NX)
   static constexpr int SEERS = 3 - 2 / NX;         // warps that look through V tiles (the rest up to warp 3)
   static constexpr int QST = HD == 64 ? 2 : 1, KST = HD == 64 ? 3 : 2;
@@ -74,7 +82,9 @@ struct WtCfg {
                        DRAIN = OFREE + 2, NBAR = DRAIN + 2;
   static constexpr int BAD_OFF = BAR_OFF + ((NBAR * 8 + 15) / 16) * 16;  // [KST][4] words: rows not finite
   static constexpr int MX_OFF = BAD_OFF + KST * 16;   // [2 tiles][2 halves][128 rows] fp32: maxima, then sums
-  static constexpr int SLOT_OFF = MX_OFF + 2 * 2 * 128 * 4;
+  static constexpr int LOST_OFF = MX_OFF + 2 * 2 * 128 * 4;  // [kLostWords] items to go through again, a bit each
+  static constexpr int STATE_OFF = LOST_OFF + kLostWords * 4;  // [20 warps][8] ints: where each role stopped
+  static constexpr int SLOT_OFF = STATE_OFF + 20 * 8 * 4;
   static constexpr int SMEM = 1024 + SLOT_OFF + 16;
   static constexpr int S_COL = 0, O_COL = 256, P_COL = OVERLAY ? 0 : 256 + 2 * HD;
   static constexpr int P_STEP = OVERLAY ? 128 : 64, P_HALF = OVERLAY ? 64 : 32;  // each half where its own S was
@@ -102,8 +112,9 @@ struct WtMaps {
 // Where in the items a CTA is: head chunk fastest, then sequence, then block of tokens (the last
 // first: long histories first). Moved on without a division.
 struct Place {
-  int it, hc, g, blk;
+  int it, hc, g, blk, k;  // k: how many items of this CTA came before
   __device__ __forceinline__ explicit Place(const WtArgs& a) {
+    k = 0;
     it = blockIdx.x;
     const int per = a.Hkv * a.chunks, r = it / per;
     hc = it - r * per;
@@ -111,6 +122,7 @@ struct Place {
     g = r - blk * a.G;
   }
   __device__ __forceinline__ void next(const WtArgs& a) {
+    ++k;
     it += gridDim.x;
     hc += a.step_hc;
     g += a.step_g;
@@ -119,6 +131,12 @@ struct Place {
     if (g >= a.G) g -= a.G, ++blk;
   }
 };
+
+// The bit of an item among those to go through again (items 2048 apart share one).
+__device__ __forceinline__ int lost_word(int k) { return (k >> 5) & (kLostWords - 1); }
+__device__ __forceinline__ bool is_lost(const volatile uint32_t* lost, int k) {
+  return (lost[lost_word(k)] >> (k & 31)) & 1u;
+}
 
 // A work item: two tiles of tq tokens from token a0 on (see the file comment for lo, sp and u).
 struct Item {
@@ -177,13 +195,18 @@ __device__ __forceinline__ bool partial(const WtArgs& a, const Item& m, int t) {
   return u0 < m.sp || k0 + 127 > m.a0 || m.last - k0 >= a.window;
 }
 
-// The tiles of this CTA's items in order, from before the first; tau numbers them (ring stages).
+// The tiles of this CTA's items (of those in `lost`, if given) in order, from before the first; tau numbers
+// them (ring stages).
 struct Walk {
   int t, tau;
   bool begun;
+  const volatile uint32_t* lost;
   Place p;
   Item m;
-  __device__ __forceinline__ explicit Walk(const WtArgs& a) : t(0), tau(-1), begun(false), p(a) { m.nt = 0; }
+  __device__ __forceinline__ Walk(const WtArgs& a, const volatile uint32_t* lost_, int tau_)
+      : t(0), tau(tau_), begun(false), lost(lost_), p(a) {
+    m.nt = 0;
+  }
   // to the next tile; false past the last
   __device__ __forceinline__ bool next(const WtArgs& a) {
     ++t;
@@ -194,7 +217,8 @@ struct Walk {
       if (begun) p.next(a);
       begun = true;
       if (p.it >= a.items) return false;
-      m = item_of(a, p);
+      m.nt = 0;
+      if (!lost || is_lost(lost, p.k)) m = item_of(a, p);
     } while (m.nt == 0);
     return true;
   }
@@ -251,47 +275,29 @@ __device__ __forceinline__ int fresh(int v) {
 }
 __device__ __forceinline__ float u2f(uint32_t u) { return __uint_as_float(u); }
 
-template <int HD>
-__global__ void __launch_bounds__(640, 1)
-    window_tc_kernel(const __grid_constant__ WtMaps maps, const __grid_constant__ WtArgs a) {
+// What the warps of a CTA do, for all its items, or (AGAIN) for those noted in shared memory. CAREFUL: references
+// are raised whenever a tile's weights add up to more than 2^12.
+template <int HD, bool CAREFUL, bool AGAIN>
+__device__ __forceinline__ void work(const WtMaps& maps, const WtArgs& a, uint8_t* const smem, const uint32_t base,
+                                     const uint32_t tmem) {
   using C = WtCfg<HD>;
-  extern __shared__ uint8_t smem_raw[];
-  const uint32_t raw = sm100::smem_u32(smem_raw);
-  const uint32_t base = (raw + 1023u) & ~1023u;
-  uint8_t* smem = smem_raw + (base - raw);
   auto bar = [&](int i) { return base + C::BAR_OFF + 8u * i; };
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::SLOT_OFF);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  volatile uint32_t* bad = reinterpret_cast<volatile uint32_t*>(smem + C::BAD_OFF);
+  volatile int* const abort_flag = reinterpret_cast<volatile int*>(smem + C::SLOT_OFF) + 1;
+  volatile uint32_t* const bad = reinterpret_cast<volatile uint32_t*>(smem + C::BAD_OFF);
+  volatile uint32_t* const lost_s = reinterpret_cast<volatile uint32_t*>(smem + C::LOST_OFF);
+  const volatile uint32_t* const lost = AGAIN ? lost_s : nullptr;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < C::NBAR; ++i) {
-      int n = 1;
-      if (i >= C::VSEEN && i < C::VSEEN + C::KST) n = 32 * C::SEERS;
-      if ((i >= C::KEMPTY && i < C::VFULL) || (i >= C::VEMPTY && i < C::VSEEN)) n = 2;
-      if ((i >= C::SFREE && i < C::OREADY) || (i >= C::OFREE && i < C::DRAIN)) n = 256;
-      sm100::mbar_init(bar(i), n);
-    }
-    *abort_flag = 0;
-    sm100::fence_barrier_init();
-    sm100::fence_proxy_async_smem();
-    sm100::tma_prefetch_desc(&maps.q);
-    sm100::tma_prefetch_desc(&maps.kv[0]);
-  }
-  if (warp == 1) sm100::tmem_alloc(sm100::smem_u32(tmem_slot), 512);
-  sm100::tc_fence_before();
-  __syncthreads();
-  sm100::tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
-  pdl_trigger();
-  pdl_wait();  // qkv comes from earlier kernels of the stream
-
+  // where the first pass stopped, for the second to go on from (the first starts from constants: the compiler
+  // makes better loops of those)
+  volatile int* const mine = reinterpret_cast<volatile int*>(smem + C::STATE_OFF) + 8 * warp;
+  constexpr bool KEEP = C::TWICE && !AGAIN;
+  auto from = [&](int i) { return AGAIN ? mine[i] : 0; };
   if (warp == 0) {
     if (lane == 0) {
       bool ok = true;
-      int nq[2] = {0, 0}, nk = 0, nv = 0;  // loads issued: Q tiles of A and B, K tiles, V tiles
-      Walk w(a);
+      // loads issued: Q tiles of A and B, K tiles, V tiles
+      int nq[2] = {from(0), from(1)}, nk = from(2), nv = from(3);
+      Walk w(a, lost, nk - 1);
       // rows u0 .. u0 + 127 of the item's keys (column col of the packed rows) into a ring tile
       auto load_tile = [&](uint32_t dst, uint32_t full, int col) {
         sm100::mbar_arrive_expect_tx(full, C::TILE);
@@ -338,6 +344,7 @@ __global__ void __launch_bounds__(640, 1)
         load_tile(base + C::V_OFF + st * C::TILE, bar(C::VFULL + st), (a.H + a.Hkv + w.m.kvh) * HD);
         ++nv;
       }
+      if (KEEP) mine[0] = nq[0], mine[1] = nq[1], mine[2] = nk, mine[3] = nv;
       if (!ok) {
         if (a.err) atomicOr(a.err, kErrTimeoutProducer);
         // let the copies already in flight land before the CTA's shared memory goes away
@@ -365,16 +372,17 @@ __global__ void __launch_bounds__(640, 1)
       Need nn[C::NX];
 #pragma unroll
       for (int i = 0; i < C::NX; ++i) {
-        nq[i] = -1, ns[i] = np[i] = no[i] = 0;
+        nq[i] = from(3 * i) - 1, ns[i] = np[i] = from(3 * i + 1), no[i] = from(3 * i + 2);
         fresh_q[i] = fresh_o[i] = true;
         p[i] = false;
         nn[i] = {0, -1};
       }
-      int st = 0, pst = 0;  // ring stages of the next key tile and of the current one
-      uint32_t ph = 0, pph = 0;
+      const int done = from(6);  // key tiles
+      int st = done % C::KST, pst = 0;  // ring stages of the next key tile and of the current one
+      uint32_t ph = (done / C::KST) & 1, pph = 0;
       auto wait = [&](int b, uint32_t parity) { return sm100::mbar_wait(bar(b), parity & 1u, abort_flag); };
       // S of the next key tile and P V of the current one, in turn
-      Walk nxt(a);
+      Walk nxt(a, lost, done - 1);
       bool cur = false, cur_first = false;  // there is a current key tile; it is an item's first
       while (ok) {
         const bool more = nxt.next(a);
@@ -451,6 +459,11 @@ __global__ void __launch_bounds__(640, 1)
           ph ^= 1u;
         }
       }
+      if (KEEP) {
+#pragma unroll
+        for (int i = 0; i < C::NX; ++i) mine[3 * i] = nq[i] + 1, mine[3 * i + 1] = np[i], mine[3 * i + 2] = no[i];
+        mine[6] = nxt.tau;
+      }
       if (!ok) {
         if (a.err) atomicOr(a.err, kErrTimeoutMma);
         sm100::mma_commit(bar(C::DRAIN + x0));
@@ -460,7 +473,7 @@ __global__ void __launch_bounds__(640, 1)
     __syncwarp();
   } else if (warp < 4) {
     bool ok = true;
-    Walk w(a);
+    Walk w(a, lost, from(0) - 1);
     while (w.next(a)) {
       const int st = w.tau % C::KST;
       ok = __all_sync(0xffffffffu, sm100::mbar_wait(bar(C::VFULL + st), (w.tau / C::KST) & 1, abort_flag));
@@ -496,6 +509,8 @@ __global__ void __launch_bounds__(640, 1)
       }
       sm100::mbar_arrive(bar(C::VSEEN + st));
     }
+    __syncwarp();
+    if (KEEP && lane == 0) mine[0] = w.tau;
     if (!ok && lane == 0 && a.err) atomicOr(a.err, kErrTimeoutEpilogue);
   } else {
     // Two threads a row, 64 columns of S each: four softmax warps per scheduler, so that one's
@@ -528,10 +543,11 @@ __global__ void __launch_bounds__(640, 1)
     };
     const float sl2 = rsqrtf(static_cast<float>(HD)) * 1.4426950408889634f;  // 1/sqrt(dh) * log2(e)
     const int hh = r / a.tq, tok = r - hh * a.tq;
-    int n = 0;    // tiles of x processed so far (barrier phases)
-    int tau = 0;  // tiles of the CTA passed
+    int n = from(0);    // tiles of x processed so far (barrier phases)
+    int tau = from(1);  // tiles of the CTA passed
     for (Place place(a); place.it < a.items; place.next(a)) {
-      int nt, token, uhi, ulo, us, late_from, early_to, part_to, part_from;
+      if (AGAIN && !is_lost(lost_s, place.k)) continue;
+      int nt, token, uhi, ulo, us, begin_to, late_from, early_to, part_to, part_from;
       Need need;
       bool idle;
       {
@@ -542,6 +558,7 @@ __global__ void __launch_bounds__(640, 1)
         const int d = m.sp - m.lo;
         token = h.b0 + tok;
         uhi = token + d, ulo = max(token - a.window + 1, m.lo) + d, us = min(a.sinks, uhi + 1);
+        begin_to = a.sinks > 0 ? 0 : h.lo1 >> 7;
         // the tiles in which some row of x sees only part (late: keys after it; early: keys that
         // left its window), and those in which some row of the item does: before part_to, from part_from
         late_from = h.hi0 - 126 <= 0 ? 0 : (h.hi0 - 126 + 127) >> 7;
@@ -554,7 +571,7 @@ __global__ void __launch_bounds__(640, 1)
       tau += nt;
       if (need.l < 0 || nt == 0) continue;
       float m_use = -3e38f, l = 0.f;  // a row that has seen nothing keeps that: its weights are 2^-inf = 0
-      bool poison = false, first = true;
+      bool poison = false;
       for (int t = 0; t <= need.l; ++t) {
         if (!needs(a, need, t)) continue;
         await(C::SFULL + x, n);
@@ -562,7 +579,6 @@ __global__ void __launch_bounds__(640, 1)
           if (!C::OVERLAY) sm100::mbar_arrive(bar(C::SFREE + x));
           if (!C::OVERLAY && n > 0) await(C::OREADY + x, n - 1);
           sm100::mbar_arrive(bar(C::PREADY + x));
-          first = false;
           ++n;
           continue;
         }
@@ -586,9 +602,11 @@ __global__ void __launch_bounds__(640, 1)
           }
         };
         float corr = 1.f, sum;
-        bool rescale = false, over = first;
+        // a tile that is the first one some row sees: gone through for its maximum (CAREFUL: of every row)
+        const bool begins = t <= begin_to;
+        bool rescale = false, over = begins && (CAREFUL || t == (fresh(us) > 0 ? 0 : fresh(ulo) >> 7));
         uint32_t pk[32];
-        for (int tries = first ? 1 : 0;; ++tries) {
+        for (int tries = begins ? 1 : 0;; ++tries) {
           if (tries > 0) {
             // the row maximum, over both halves
             float mxp[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -615,8 +633,8 @@ __global__ void __launch_bounds__(640, 1)
               mx = fmaxf(over ? mx : m_use, other == other ? other : m_use);
               if (mx > m_use) {
                 corr = ex2((m_use - mx) * sl2);
+                rescale = m_use > -3e38f;  // else O is 0
                 m_use = mx;
-                rescale = !first;
               }
             }
           }
@@ -645,8 +663,9 @@ __global__ void __launch_bounds__(640, 1)
             }
           }
           sum = (sp[0] + sp[1]) + (sp[2] + sp[3]);
+          if (!CAREFUL || tries > 0) break;
           over = !(sum <= 4096.f);  // NaN too: gone through once more, to no effect
-          if (tries > 0 || !meet_any(over)) break;
+          if (!meet_any(over)) break;
         }
         sm100::tc_fence_before();
         if (!C::OVERLAY) sm100::mbar_arrive(bar(C::SFREE + x));
@@ -685,7 +704,6 @@ __global__ void __launch_bounds__(640, 1)
         sm100::tmem_wait_st();
         sm100::tc_fence_before();
         sm100::mbar_arrive(bar(C::PREADY + x));
-        first = false;
         ++n;
       }
       // end of the item: the row's sum over both halves, and O after its last P V, normalised and
@@ -716,11 +734,85 @@ __global__ void __launch_bounds__(640, 1)
             store32_16(dst + 32 * oc, v);
           }
         }
+        // Weights and sums have fp32's range, so a reference that is too low does no harm until a weight or O
+        // leaves it; the item is then gone through again.
+        if (!CAREFUL && !idle && __any_sync(0xffffffffu, l > 4096.f)) {
+          float z = 0.f;
+#pragma unroll 1
+          for (int oc = 0; oc < HD / 32; ++oc) {
+            uint32_t o[16];
+            sm100::tmem_ld16(tO + 16 * oc, o);
+            sm100::tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) z = fmaf(u2f(o[i]), 0.f, z);  // 0 * x is NaN for infinities and NaN
+          }
+          if (row_out && (l > 1.152921504606847e18f || (l > 4096.f && z != 0.f)))
+            atomicOr(const_cast<uint32_t*>(lost_s) + lost_word(place.k), 1u << (place.k & 31));
+        }
       }
       sm100::tc_fence_before();
       sm100::mbar_arrive_relaxed(bar(C::OFREE + x));
     }
+    __syncwarp();
+    if (KEEP && lane == 0) mine[0] = n, mine[1] = tau;
     if (dead && lane == 0 && a.err) atomicOr(a.err, kErrTimeoutEpilogue);
+  }
+}
+// Out of line, so that its registers are not the first pass's
+template <int HD>
+__device__ __noinline__ void work_again(const WtMaps& maps, const WtArgs& a, uint8_t* smem, uint32_t base, uint32_t tmem) {
+  work<HD, true, true>(maps, a, smem, base, tmem);
+}
+
+template <int HD>
+__global__ void __launch_bounds__(640, 1)
+    window_tc_kernel(const __grid_constant__ WtMaps maps, const __grid_constant__ WtArgs a) {
+  using C = WtCfg<HD>;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = sm100::smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* smem = smem_raw + (base - raw);
+  auto bar = [&](int i) { return base + C::BAR_OFF + 8u * i; };
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::SLOT_OFF);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  volatile uint32_t* lost_s = reinterpret_cast<volatile uint32_t*>(smem + C::LOST_OFF);
+  volatile int* state = reinterpret_cast<volatile int*>(smem + C::STATE_OFF);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::NBAR; ++i) {
+      int n = 1;
+      if (i >= C::VSEEN && i < C::VSEEN + C::KST) n = 32 * C::SEERS;
+      if ((i >= C::KEMPTY && i < C::VFULL) || (i >= C::VEMPTY && i < C::VSEEN)) n = 2;
+      if ((i >= C::SFREE && i < C::OREADY) || (i >= C::OFREE && i < C::DRAIN)) n = 256;
+      sm100::mbar_init(bar(i), n);
+    }
+    *abort_flag = 0;
+    for (int i = 0; i < kLostWords; ++i) lost_s[i] = 0;
+    for (int i = 0; i < 20 * 8; ++i) state[i] = 0;
+    sm100::fence_barrier_init();
+    sm100::fence_proxy_async_smem();
+    sm100::tma_prefetch_desc(&maps.q);
+    sm100::tma_prefetch_desc(&maps.kv[0]);
+  }
+  if (warp == 1) sm100::tmem_alloc(sm100::smem_u32(tmem_slot), 512);
+  sm100::tc_fence_before();
+  __syncthreads();
+  sm100::tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  pdl_trigger();
+  pdl_wait();  // qkv comes from earlier kernels of the stream
+
+  work<HD, !C::TWICE, false>(maps, a, smem, base, tmem);
+  if constexpr (C::TWICE) {
+    sm100::tc_fence_before();
+    __syncthreads();
+    uint32_t again = 0;
+    for (int i = lane; i < kLostWords; i += 32) again |= lost_s[i];
+    if (!*abort_flag && __any_sync(0xffffffffu, again != 0)) {  // the same for every warp
+      sm100::tc_fence_after();
+      work_again<HD>(maps, a, smem, base, tmem);
+    }
   }
 
   sm100::tc_fence_before();

@@ -483,6 +483,33 @@ def test_window_attention_keeps_masked_values_out(cuda_ok, dtype, bad, dh):
 
 
 @gpu
+@pytest.mark.parametrize("dtype,dh,sinks", [("bf16", 64, 0), ("bf16", 64, 4), ("bf16", 128, 0), ("bf16", 128, 4),
+                                            ("f32", 64, 4)])
+def test_window_attention_of_scores_that_rise_far_above_the_first(cuda_ok, dtype, dh, sinks):
+    """Scores far above those of the first keys a row sees: by 2^184 in one head, by 2^20 with values near the
+    type's end in another, by a little again and again in a third; the fourth has none of that."""
+    H, Hkv, G, M, window = 8, 4, 2, 900, 300
+    qkv = normal(51, (G, M, (H + 2 * Hkv) * dh), dtype).reshape(G, M, H + 2 * Hkv, dh)
+    a = dh ** -0.5
+    qkv[:, :, :6] = 8.0  # heads of the first three key heads: score 8 sqrt(dh) times a key's common value
+    tok = torch.arange(M, device="cuda")
+    up = lambda lo, hi: torch.where(tok < 420, lo, hi).to(qkv.dtype)[:, None]
+    qkv[:, :, H] = up(-8 * a, 8 * a)  # -64 and 64
+    qkv[:, :, H + 1] = up(0.0, 1.75 * a)  # 0 and 14
+    qkv[:, :, H + Hkv + 1] *= 1e36
+    qkv[:, :, H + 2] = (tok.to(qkv.dtype) / 32 * a)[:, None]  # a quarter of a unit per token
+    qkv = qkv.reshape(G, M, -1)
+    out = torch.zeros(G, M, H * dh, dtype=TORCH[dtype], device="cuda")
+    rmt.rmt_attention_window(qkv, out, G, M, H, Hkv, dh, window, sinks, dtype=dtype)
+    rmt.rmt_sync(None)
+    got, x = f64(out).reshape(G, M, H, dh), f64(qkv).reshape(G, M, H + 2 * Hkv, dh)
+    for g in range(G):
+        ref = attend_ref(x[g, :, :H], x[g, :, H:H + Hkv], x[g, :, H + Hkv:], np.arange(M), window, sinks)
+        for h in range(H):
+            check_attention(got[g, :, h], ref[:, h], np.abs(x[g, :, H + Hkv + h // 2]).max(), dtype)
+
+
+@gpu
 @pytest.mark.parametrize("dtype,dh", [("bf16", 32), ("f32", 64), ("bf16", 64), ("bf16", 128), ("f32", 128)])
 def test_window_attention_shows_a_value_that_is_not_finite_whatever_its_weight(cuda_ok, dtype, dh):
     """Token 7's weight is below 2^-1000 in every row but its own; its value is infinite."""
