@@ -716,14 +716,27 @@ __device__ __forceinline__ void work(const WtMaps& maps, const WtArgs& a, uint8_
       }
       await(C::OREADY + x, n - 1);
       sm100::tc_fence_after();
-      const float inv = poison ? NAN : 1.f / l;
+      const bool lost_row = !CAREFUL && l > 1.152921504606847e18f;
+      const float inv = poison || lost_row ? NAN : 1.f / l;
       {
         const Item m = item_of(a, place);  // again, rather than in registers through the tiles
-        const bool row_out = hh < m.nh && token < m.T;
+        bool row_out = hh < m.nh && token < m.T;
         bf16* const dst = static_cast<bf16*>(a.out) +
                           ((static_cast<size_t>(m.g) * a.M + token) * a.H + m.h0 + hh) * HD + HD / 2 * half;
 #pragma unroll 1
         for (int oc = 0; oc < (idle ? 0 : HD / 64); ++oc) {
+          // the second time only rows that are not finite yet: the others' bits do not depend on their neighbours
+          if (AGAIN && row_out) {
+            bool open = false;
+            for (int i = 0; i < 4; ++i) {
+              const uint4 w = *reinterpret_cast<const uint4*>(dst + 32 * oc + 8 * i);
+              const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                open |= (ws[k] & 0x7F80u) == 0x7F80u || (ws[k] & 0x7F800000u) == 0x7F800000u;
+            }
+            row_out = open;
+          }
           uint32_t o[32];
           sm100::tmem_ld32(tO + 32 * oc, o);
           sm100::tmem_wait_ld();
@@ -746,7 +759,7 @@ __device__ __forceinline__ void work(const WtMaps& maps, const WtArgs& a, uint8_
 #pragma unroll
             for (int i = 0; i < 16; ++i) z = fmaf(u2f(o[i]), 0.f, z);  // 0 * x is NaN for infinities and NaN
           }
-          if (row_out && (l > 1.152921504606847e18f || (l > 4096.f && z != 0.f)))
+          if (row_out && (lost_row || (l > 4096.f && z != 0.f)))
             atomicOr(const_cast<uint32_t*>(lost_s) + lost_word(place.k), 1u << (place.k & 31));
         }
       }

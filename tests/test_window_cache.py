@@ -510,6 +510,30 @@ def test_window_attention_of_scores_that_rise_far_above_the_first(cuda_ok, dtype
 
 
 @gpu
+@pytest.mark.parametrize("dtype,dh", [("bf16", 64), ("bf16", 128), ("f32", 64)])
+@pytest.mark.parametrize("sinks", [0, 4])
+def test_window_attention_keeps_a_rows_bits_whatever_later_scores_are(cuda_ok, dtype, dh, sinks):
+    """Scores that rise by a quarter per token, and the same with a jump by 2^184 from token 420 on: the rows
+    before it, in the same query tiles as rows that see it, come out alike to the bit."""
+    H, Hkv, M, window = 4, 2, 700, 300
+    qkv = normal(52, (1, M, H + 2 * Hkv, dh), dtype)
+    a = dh ** -0.5
+    tok = torch.arange(M, device="cuda")
+    qkv[:, :, :H] = 8.0
+    qkv[:, :, H:H + Hkv] = ((tok % 256).to(qkv.dtype) / 32 * a)[:, None, None]
+    outs = []
+    for jump in (0.0, 16.0):
+        x = qkv.clone()
+        x[:, 420:, H] += jump * a
+        out = torch.zeros(1, M, H * dh, dtype=TORCH[dtype], device="cuda")
+        rmt.rmt_attention_window(x.reshape(1, M, -1), out, 1, M, H, Hkv, dh, window, sinks, dtype=dtype)
+        rmt.rmt_sync(None)
+        assert torch.isfinite(out).all()
+        outs.append(out.reshape(M, H, dh))
+    assert torch.equal(outs[0][:420], outs[1][:420]) and torch.equal(outs[0][:, 2:], outs[1][:, 2:])
+
+
+@gpu
 @pytest.mark.parametrize("dtype,dh", [("bf16", 32), ("f32", 64), ("bf16", 64), ("bf16", 128), ("f32", 128)])
 def test_window_attention_shows_a_value_that_is_not_finite_whatever_its_weight(cuda_ok, dtype, dh):
     """Token 7's weight is below 2^-1000 in every row but its own; its value is infinite."""
