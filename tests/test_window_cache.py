@@ -510,6 +510,32 @@ def test_window_attention_of_scores_that_rise_far_above_the_first(cuda_ok, dtype
 
 
 @gpu
+@pytest.mark.parametrize("dh,M,G", [(64, 900, 8), (64, 6000, 8), (64, 700, 33), (128, 900, 8)])
+def test_window_attention_of_many_sequences_whose_scores_rise(cuda_ok, dh, M, G):
+    """The same sequence G times, every other one without its jump by 2^184, gives what it gives alone, to the bit;
+    and again."""
+    H, Hkv, window, sinks = 16, 8, 300, 2
+    qkv = normal(53, (1, M, H + 2 * Hkv, dh), "bf16").repeat(2, 1, 1, 1)
+    qkv[:, :, :H] = 8.0
+    a = dh ** -0.5
+    qkv[:, :, H:H + Hkv] = -8 * a
+    qkv[0, M // 2:, H:H + Hkv:3] = 8 * a
+    alone = []
+    for x in qkv:
+        out = torch.zeros(1, M, H * dh, dtype=torch.bfloat16, device="cuda")
+        rmt.rmt_attention_window(x.reshape(1, M, -1), out, 1, M, H, Hkv, dh, window, sinks)
+        alone.append(out)
+    batch = qkv.reshape(2, M, -1)[torch.arange(G, device="cuda") % 2].contiguous()
+    for _ in range(2):
+        out = torch.zeros(G, M, H * dh, dtype=torch.bfloat16, device="cuda")
+        rmt.rmt_attention_window(batch, out, G, M, H, Hkv, dh, window, sinks)
+        rmt.rmt_sync(None)
+        assert torch.isfinite(out).all()
+        for g in range(G):
+            assert torch.equal(out[g], alone[g % 2][0]), g
+
+
+@gpu
 @pytest.mark.parametrize("dtype,dh", [("bf16", 64), ("bf16", 128), ("f32", 64)])
 @pytest.mark.parametrize("sinks", [0, 4])
 def test_window_attention_keeps_a_rows_bits_whatever_later_scores_are(cuda_ok, dtype, dh, sinks):
