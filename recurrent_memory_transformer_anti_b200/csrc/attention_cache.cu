@@ -545,7 +545,8 @@ __global__ void __launch_bounds__(32 * Shape<DH, T, NT>::WARPS, 1) cache_attn_ke
               top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
               top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
               top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-              top = fmaxf(top, m[j][c]);
+              // this row's own: whether another row's is raised does not show in its bits
+              if (!((top - m[j][c]) * rs[j][c] > 8.f)) top = m[j][c];
               const float ref = top == -INFINITY ? 0.f : top;  // nothing seen yet: weights 2^-inf = 0
               corr[c] = ex2((m[j][c] - ref) * rs[j][c]);
               m[j][c] = top;

@@ -368,6 +368,24 @@ def test_cache_attention_of_queries_that_are_not_finite(cuda_ok):
 
 
 @gpu
+@pytest.mark.parametrize("lens", [[700], [5000]])
+def test_cache_attention_of_a_row_does_not_depend_on_the_other_rows(cuda_ok, lens):
+    """Other heads' queries, and another token's, change: the row's bits do not."""
+    dh, H, Hkv = 64, 8, 2
+    s = Setup(lens, Hkv, dh)
+    s.fill(61, "bf16")
+    q = normal(62, (1, 2, H, dh), "bf16")
+    want = s.attend(q.reshape(1, 2, -1), 2, H, 0, 0, "bf16").reshape(2, H, dh)
+    for t, h in ((0, 0), (1, 5), (1, 7)):
+        x = q * 40
+        x[0, t, h] = q[0, t, h]
+        got = s.attend(x.reshape(1, 2, -1), 2, H, 0, 0, "bf16").reshape(2, H, dh)
+        rmt.rmt_sync(None)
+        assert torch.equal(got[t, h], want[t, h])
+        assert not torch.equal(got, want)
+
+
+@gpu
 @pytest.mark.parametrize("n_q,window", [(1, 0), (2, 100)])
 def test_rows_of_unused_slots_give_zeros_whatever_they_hold(cuda_ok, n_q, window):
     s = Setup([0, 3000, 1], 1, 64)
