@@ -444,7 +444,8 @@ size_t rmt_attention_cache_workspace(const rmt_cache* c, int32_t n_q, int32_t H,
  * first) over the pages. q: row i of sequence b starts at element (b*n_q + i)*ldq and holds H*head_dim
  * values; out [n_seqs, n_q, H*head_dim]; both in dtype (RMT_F32 or RMT_BF16). Keys and values are
  * the ones rmt_cache_read gives; softmax and sums in fp32. A row that sees no key (a
- * negative position) gives zeros. The workspace needs no initial value and may be used again by
+ * negative position) gives zeros. A token that no row of the call sees need never have been
+ * written, and a page without any other is not looked up. The workspace needs no initial value and may be used again by
  * later calls on the same stream; calls that may overlap (two streams, two graphs replayed at
  * once) need one each. Equal calls give equal bits. */
 rmt_status rmt_attention_cache(const rmt_cache* c, const void* q, int64_t ldq, void* out, int32_t n_q, int32_t H,

@@ -1,0 +1,53 @@
+"""Calls at the edges of the windowed attention and the 4-bit cache: tokens that were never written, row counts
+past the grid's 32 bits, extreme numbers, the shared list of units, other devices."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+from recurrent_memory_transformer_anti_b200 import rmt
+from test_window_cache import TORCH, Setup, attend_ref, check_attention, decode_ref, encode_ref, f64, normal, visible
+
+gpu = pytest.mark.gpu
+
+
+# ------------------------------------------------------------ tokens that nobody sees, never written
+
+HALF = [  # dh, H, Hkv, lens, n_q, window, sinks; at most 32 units an item, and more
+    (64, 8, 2, [300, 0, 70], 1, 100, 0), (64, 8, 2, [300, 40], 1, 100, 5), (32, 4, 2, [333], 3, 90, 70),
+    (128, 4, 2, [300, 129], 2, 77, 1), (128, 16, 1, [500], 1, 33, 33), (64, 12, 1, [1000, 200], 5, 1, 3),
+    (64, 8, 2, [5000, 300, 0], 1, 3001, 0), (64, 8, 1, [5000, 5], 3, 2900, 70), (32, 4, 2, [5100], 2, 2999, 3),
+    (128, 4, 2, [2500, 1700], 2, 1300, 37), (128, 24, 2, [2600], 3, 1500, 1)]
+
+
+@gpu
+@pytest.mark.parametrize("fill", [0xFF, 0xF8])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("dh,H,Hkv,lens,n_q,window,sinks", HALF)
+def test_cache_attention_needs_no_tokens_that_no_row_sees(cuda_ok, dtype, dh, H, Hkv, lens, n_q, window, sinks, fill):
+    """Only the sinks and what the rows' windows reach are ever written; every other byte of the pages stands for
+    NaN (0xFF) or infinity (0xF8) where it is a scale."""
+    n, M = len(lens), max(lens)
+    s = Setup(lens, Hkv, dh, seed=n, fill=fill)
+    k, v = (normal(70 + i, (n, M, Hkv * dh), dtype) for i in (0, 1))  # row t: token t
+    first = [max(0, t - n_q - window + 1) for t in lens]
+    rows = max(t - f for t, f in zip(lens, first))
+    newest = [torch.zeros(n, max(rows, 1), Hkv * dh, dtype=TORCH[dtype], device="cuda") for _ in range(2)]
+    for b in range(n):
+        for x, src in zip(newest, (k, v)):
+            x[b, :lens[b] - first[b]] = src[b, first[b]:lens[b]]
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    rmt.rmt_cache_write(s.cache, *newest, max(rows, 1), n_new=i32([t - f for t, f in zip(lens, first)]), dtype=dtype)
+    if sinks:
+        head = i32([min(sinks, t) for t in lens])
+        c = rmt.rmt_cache(s.pages, s.table, head, Hkv, dh)
+        rmt.rmt_cache_write(c, k[:, :sinks].contiguous(), v[:, :sinks].contiguous(), min(sinks, M), n_new=head, dtype=dtype)
+    q = normal(72, (n, n_q, H * dh), dtype)
+    got = f64(s.attend(q, n_q, H, window, sinks, dtype))
+    rmt.rmt_sync(None)
+    held = [decode_ref(*encode_ref(f64(x).reshape(n, M, Hkv, dh))) for x in (k, v)]
+    for b in range(n):
+        kk, vv = (x[b, :lens[b]] for x in held)
+        ref = attend_ref(f64(q)[b].reshape(n_q, H, dh), kk, vv, np.arange(lens[b] - n_q, lens[b]), window, sinks)
+        check_attention(got[b].reshape(n_q, H, dh), ref, np.abs(vv).max() if vv.size else 0.0, dtype)
