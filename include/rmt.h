@@ -426,7 +426,7 @@ size_t rmt_cache_page_bytes(int32_t n_kv_heads, int32_t head_dim);
  * at most M), or NULL (M each). Row i < n_new[b] becomes token lens[b] - n_new[b] + i; rows whose
  * token would be negative (an unused slot) are skipped. No two rows of one call may fall on the
  * same token of a page. dtype RMT_F32 or RMT_BF16; k, v and the bytes of ld multiples of 16;
- * n_seqs * M below 2^31. */
+ * n_seqs * M below 2^31, and with n_kv_heads * head_dim at most 2^37. */
 rmt_status rmt_cache_write(const rmt_cache* c, const void* k, const void* v, int64_t ld, int32_t M,
                            const int32_t* n_new, rmt_dtype dtype, void* stream);
 

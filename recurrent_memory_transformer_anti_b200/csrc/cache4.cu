@@ -20,6 +20,8 @@ namespace {
 
 using cache4::kPage;
 
+constexpr uint32_t kWarps = 8;  // of a CTA
+
 // n / d of numbers below 2^31: (n * m) >> s, m = 2^s / d rounded up and below 2^32 + 1, so that what
 // rounding adds, n / 2^s at most, does not reach the next integer.
 struct Divider {
@@ -144,11 +146,11 @@ __device__ __forceinline__ uint32_t encode16(const Raw<__nv_bfloat16>& r, uint32
 }
 
 template <int DH, typename T, int COLS>
-__global__ void __launch_bounds__(256) cache_write_kernel(const CacheRowsArgs a, const Deal d) {
+__global__ void __launch_bounds__(32 * kWarps) cache_write_kernel(const CacheRowsArgs a, const Deal d) {
   pdl_trigger();
   pdl_wait();
   using L = cache4::Layout<DH>;
-  const uint32_t warp = (blockIdx.x * blockDim.x + threadIdx.x) >> 5;
+  const uint32_t warp = blockIdx.x * kWarps + (threadIdx.x >> 5);  // the threads' numbers may pass 32 bits
   if (warp >= d.warps) return;
   const uint32_t group = d.by_cols(warp);
   uint32_t head = (warp - group * d.cols) * COLS;
@@ -205,11 +207,11 @@ __device__ __forceinline__ void decode8(__nv_bfloat16* dst, uint32_t w, uint32_t
 }
 
 template <int DH, typename T, int COLS>
-__global__ void __launch_bounds__(256) cache_read_kernel(const CacheRowsArgs a, const Deal d) {
+__global__ void __launch_bounds__(32 * kWarps) cache_read_kernel(const CacheRowsArgs a, const Deal d) {
   pdl_trigger();
   pdl_wait();
   using L = cache4::Layout<DH>;
-  const uint32_t warp = (blockIdx.x * blockDim.x + threadIdx.x) >> 5;
+  const uint32_t warp = blockIdx.x * kWarps + (threadIdx.x >> 5);  // the threads' numbers may pass 32 bits
   if (warp >= d.warps) return;
   const uint32_t group = d.by_cols(warp);
   uint32_t head = (warp - group * d.cols) * COLS;
@@ -236,11 +238,12 @@ __global__ void __launch_bounds__(256) cache_read_kernel(const CacheRowsArgs a, 
 template <int DH, typename T, int COLS>
 cudaError_t launch_cols(const CacheRowsArgs& a, bool write, long long groups, cudaStream_t st) {
   const uint32_t cols = 2u * a.c.Hkv / COLS;
-  const long long blocks = (groups * cols + 7) / 8;
-  if (blocks > 0x07ffffffLL) return cudaErrorInvalidValue;  // the threads' numbers are 32 bits
-  const Deal d{cols, static_cast<uint32_t>(groups * cols), Divider(cols), Divider(a.M)};
+  const long long warps = groups * cols;
+  if (warps > 0x7fffffffLL) return cudaErrorInvalidValue;  // Divider's range; the C entries let 2^30 through
+  const long long blocks = (warps + kWarps - 1) / kWarps;
+  const Deal d{cols, static_cast<uint32_t>(warps), Divider(cols), Divider(a.M)};
   const cudaError_t e = launch_pdl(write ? cache_write_kernel<DH, T, COLS> : cache_read_kernel<DH, T, COLS>,
-                                   dim3(static_cast<unsigned>(blocks)), dim3(256), 0, st, a, d);
+                                   dim3(static_cast<unsigned>(blocks)), dim3(32 * kWarps), 0, st, a, d);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 

@@ -73,6 +73,9 @@ rmt_status cache_rows(const rmt_cache* c, const void* k, const void* v, int64_t 
   if (const char* why = cache_problem(c)) return fail(RMT_EINVAL, why);
   if (!k || !v) return fail(RMT_EINVAL, "null pointer");
   if (M <= 0 || int64_t(c->n_seqs) * M > INT_MAX) return fail(RMT_EINVAL, "M must be positive, n_seqs * M below 2^31");
+  // 8 channels a thread: no more than 2^30 warps, and their heads rounded up
+  if (int64_t(c->n_seqs) * M * (int64_t(c->n_kv_heads) * c->head_dim) > (int64_t(1) << 37))
+    return fail(RMT_EINVAL, "n_seqs * M * n_kv_heads * head_dim must be at most 2^37");
   if (dtype != RMT_F32 && dtype != RMT_BF16) return fail(RMT_EINVAL, "dtype must be RMT_F32 or RMT_BF16");
   const int64_t es = dtype == RMT_BF16 ? 2 : 4;
   if (ld < int64_t(c->n_kv_heads) * c->head_dim) return fail(RMT_EINVAL, "ld is below n_kv_heads * head_dim");

@@ -51,3 +51,45 @@ def test_cache_attention_needs_no_tokens_that_no_row_sees(cuda_ok, dtype, dh, H,
         kk, vv = (x[b, :lens[b]] for x in held)
         ref = attend_ref(f64(q)[b].reshape(n_q, H, dh), kk, vv, np.arange(lens[b] - n_q, lens[b]), window, sinks)
         check_attention(got[b].reshape(n_q, H, dh), ref, np.abs(vv).max() if vv.size else 0.0, dtype)
+
+
+# ------------------------------------------------------------------------- many rows in one call
+
+@gpu
+def test_cache_rows_whose_threads_pass_32_bits(cuda_ok):
+    """A padded batch of 34 (written) and 17 (read) sequences of 2^23 rows, of which each has three: 16 and 8 rows a
+    CTA, 256 threads a CTA, so that sequences from 32 and 16 on begin behind thread 2^32."""
+    dh, M, n, new = 128, 2 ** 23, 34, 3
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < 2 * n * M * dh + 2 ** 32:
+        pytest.skip("needs 77 GB")
+    x = torch.empty(n, M, dh, dtype=torch.bfloat16, device="cuda")
+    x[:, :new] = normal(1, (n, new, dh), "bf16")
+    codes, byte = encode_ref(f64(x[:, :new]))
+    s = Setup([5] * n, 1, dh, fill=0xA5)
+    n_new = torch.full((n,), new, dtype=torch.int32, device="cuda")
+    rmt.rmt_cache_write(s.cache, x, x, M, n_new=n_new)
+    rmt.rmt_sync(None)
+    parts, page = s.halves(), s.table.cpu().numpy()[:, 0]
+    for i in (0, 2):
+        np.testing.assert_array_equal(parts[i][page, 0, 2:5], codes[..., 0::2] | (codes[..., 1::2] << 4))
+        np.testing.assert_array_equal(parts[i + 1][page, 0, 2:5], byte)
+    x[:, :new + 1] = -77.0
+    half = n // 2
+    first = rmt.rmt_cache(s.pages, s.table[:half].contiguous(), s.lens[:half].contiguous(), 1, dh)
+    rmt.rmt_cache_read(first, x[:half], x[half:], M, n_new=n_new)
+    rmt.rmt_sync(None)
+    for got in (x[:half], x[half:]):
+        np.testing.assert_array_equal(f64(got[:, :new]), decode_ref(codes, byte)[:half])
+        assert (got[:, new] == -77.0).all()
+    del x, got
+    torch.cuda.empty_cache()
+
+
+def test_more_rows_than_any_device_holds_are_refused():
+    c = rmt.rmt_cache_struct(256, 256, 256, 4, 2 ** 10, 2, 4096, 128)
+    lib = rmt.lib()
+    for fn in (lib.rmt_cache_write, lib.rmt_cache_read):
+        for M in (2 ** 8 + 1, 2 ** 20):
+            assert fn(ctypes.byref(c), 256, 256, 4096 * 128, M, None, 1, None) == rmt.RMT_EINVAL
+            assert "2^37" in rmt.rmt_last_error()
