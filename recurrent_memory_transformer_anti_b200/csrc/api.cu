@@ -1473,15 +1473,15 @@ rmt_status rmt_get_trace(rmt_handle* h, int32_t* out_dls, size_t cap) {
 }
 
 rmt_status rmt_sync(rmt_handle* h, void* stream) {
+  // the device whose error word is meant: the handle's, or the stream's (NULL: a stream of the current device)
+  int dev = h ? h->dev : -1;
+  if (!h && stream) RMT_CUDA(cudaStreamGetDevice(static_cast<cudaStream_t>(stream), &dev));
+  DeviceGuard guard(dev);
   int* err = nullptr;
-  if (h) {
+  if (h)
     err = h->err;
-  } else {
-    const Cell* cells = nullptr;
-    rmt_status s = device_scratch(1, &cells, &err);
-    if (s != RMT_OK) return s;
-  }
-  DeviceGuard guard(h ? h->dev : -1);
+  else
+    RMT_TRY(current_error_word(&err));
   RMT_CUDA(cudaStreamSynchronize(static_cast<cudaStream_t>(stream)));
   RMT_CUDA(cudaGetLastError());
   int word = 0;

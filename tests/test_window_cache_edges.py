@@ -93,3 +93,39 @@ def test_more_rows_than_any_device_holds_are_refused():
         for M in (2 ** 8 + 1, 2 ** 20):
             assert fn(ctypes.byref(c), 256, 256, 4096 * 128, M, None, 1, None) == rmt.RMT_EINVAL
             assert "2^37" in rmt.rmt_last_error()
+
+
+# ------------------------------------------------------------------------------ what rmt_sync reports
+
+def met_bad_page(device="cuda", stream=None):
+    """Reads a row through a table entry that is no page."""
+    table, lens = (torch.full(sh, val, dtype=torch.int32, device=device) for sh, val in (((1, 1), 9), ((1,), 1)))
+    c = rmt.rmt_cache(torch.zeros(4608, dtype=torch.uint8, device=device), table, lens, 1, 64)
+    k = torch.zeros(1, 1, 64, dtype=torch.bfloat16, device=device)
+    torch.cuda.synchronize(device)
+    rmt.rmt_cache_read(c, k, k.clone(), 1, stream=stream)
+
+
+def sync_error(stream=None):
+    with pytest.raises(rmt.RmtError) as e:
+        rmt.rmt_sync(None, stream=stream)
+    rmt.rmt_sync(None, stream=stream)  # the word was cleared
+    return e.value
+
+
+@gpu
+def test_sync_reports_on_the_stream_it_is_given(cuda_ok):
+    for stream in (torch.cuda.Stream(), torch.cuda.default_stream()):
+        met_bad_page(stream=stream)
+        assert sync_error(stream).status == rmt.RMT_EINVAL
+
+
+@gpu
+def test_sync_reports_what_a_device_met_that_is_not_the_current_one(cuda_ok):
+    if torch.cuda.device_count() < 2:
+        pytest.skip("needs two GPUs")
+    with torch.cuda.device(0):
+        stream = torch.cuda.Stream(1)
+        met_bad_page("cuda:1", stream)
+        rmt.rmt_sync(None)  # device 0 met nothing
+        assert sync_error(stream).status == rmt.RMT_EINVAL
