@@ -210,12 +210,13 @@ rmt_status rmt_schedule_table_batch(int32_t n_layers, int32_t batch, const int32
  * Synchronizes the device. RMT_ESTATE before the first forward. */
 rmt_status rmt_get_trace(rmt_handle* h, int32_t* out_dls, size_t cap);
 
-/* Wait for `stream`, then report (and clear) the handle's device error word: RMT_ETIMEOUT
- * if a bounded device wait gave up, RMT_ERANGE if the only fault since the last check is an
- * f16 operand overflow (see rmt_dtype), RMT_EDEBUG if a bounds check of the debug build
- * failed (see rmt_bounds_selftest), RMT_ECUDA on a CUDA error. With h == NULL the error word
- * of the kernel-level entry points on the stream's device is checked (stream == NULL: on the
- * current device), whatever the current device is. */
+/* Wait for `stream`, then report (and clear) the handle's device error word. If it holds
+ * several faults the status is the first of: RMT_EDEBUG if a bounds check of the debug build
+ * failed (see rmt_bounds_selftest), RMT_ETIMEOUT if a bounded device wait gave up, RMT_EINVAL if a
+ * length or page table entry did not fit its cache, RMT_ERANGE for an f16 operand overflow (see
+ * rmt_dtype); rmt_last_error() names all of them. RMT_ECUDA on a CUDA error. With h == NULL the
+ * error word of the kernel-level entry points on the stream's device is checked (stream == NULL:
+ * on the current device), whatever the current device is. */
 rmt_status rmt_sync(rmt_handle* h, void* stream);
 
 /* Check of the failure path: one CTA waits on an mbarrier that nothing signals, with the

@@ -1488,18 +1488,29 @@ rmt_status rmt_sync(rmt_handle* h, void* stream) {
   RMT_CUDA(cudaMemcpy(&word, err, sizeof(int), cudaMemcpyDeviceToHost));
   if (word) {
     RMT_CUDA(cudaMemset(err, 0, sizeof(int)));
-    if (word & kErrBounds)
-      return fail(RMT_EDEBUG, "a kernel's bounds check failed: a cell index fell outside its buffers (error word " +
-                                  std::to_string(word) + ")");
-    if (word == kErrPage)
-      return fail(RMT_EINVAL,
-                  "a cache operator met a length or a page table entry outside its cache; the rows concerned were "
-                  "neither read nor written");
-    if (word == kErrF16Range)
-      return fail(RMT_ERANGE,
-                  "a value of magnitude 65520 or more was stored as an f16 tensor-core operand (bf16 mode): the "
-                  "outputs of this forward are not valid");
-    return fail(RMT_ETIMEOUT, "a bounded device wait gave up (error word " + std::to_string(word) + ")");
+    // one status, the gravest; the message names all that the word holds
+    const struct {
+      int bits;
+      rmt_status st;
+      const char* what;
+    } faults[] = {
+        {kErrBounds, RMT_EDEBUG, "a kernel's bounds check failed: a cell index fell outside its buffers"},
+        {~(kErrBounds | kErrPage | kErrF16Range), RMT_ETIMEOUT, "a bounded device wait gave up"},
+        {kErrPage, RMT_EINVAL,
+         "a cache operator met a length or a page table entry outside its cache; the rows concerned were neither read "
+         "nor written"},
+        {kErrF16Range, RMT_ERANGE,
+         "a value of magnitude 65520 or more was stored as an f16 tensor-core operand (bf16 mode): the outputs of this "
+         "forward are not valid"},
+    };
+    rmt_status st = RMT_OK;
+    std::string msg;
+    for (const auto& f : faults) {
+      if (!(word & f.bits)) continue;
+      if (st == RMT_OK) st = f.st;
+      msg += (msg.empty() ? "" : "; ") + std::string(f.what);
+    }
+    return fail(st, msg + " (error word " + std::to_string(word) + ")");
   }
   return RMT_OK;
 }

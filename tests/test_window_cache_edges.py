@@ -129,3 +129,12 @@ def test_sync_reports_what_a_device_met_that_is_not_the_current_one(cuda_ok):
         met_bad_page("cuda:1", stream)
         rmt.rmt_sync(None)  # device 0 met nothing
         assert sync_error(stream).status == rmt.RMT_EINVAL
+
+
+@gpu
+def test_sync_names_every_fault_of_the_word(cuda_ok):
+    met_bad_page()
+    rmt.rmt_wait_selftest(100)
+    e = sync_error()
+    assert e.status == rmt.RMT_ETIMEOUT
+    assert "wait gave up" in str(e) and "page table entry" in str(e)
