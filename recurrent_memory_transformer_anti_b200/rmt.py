@@ -168,6 +168,19 @@ def _ptr32(x, count=None):
     return _ptr(x)
 
 
+def _same_device(device: int, *arrays) -> None:
+    """Refuse tensors that are not on `device` (an index; -1 is host memory): a kernel would fault on their
+    addresses. Addresses and None are taken as they are."""
+    for x in arrays:
+        if x is not None and x.__class__ is not int:
+            try:
+                if x.get_device() == device:
+                    continue
+            except AttributeError:  # a numpy array
+                pass
+            raise ValueError("all tensors of a call must be on the device of its pages (or qkv)")
+
+
 def _whole(x, count: int, dtype: str):
     """Address of a contiguous tensor of at least `count` values (an address is taken as it is)."""
     if x is None or isinstance(x, int):
@@ -406,6 +419,8 @@ def rmt_rmsnorm(x, g, y, rows, d, eps, dtype="f32", stream=None) -> None:
 
 def rmt_attention_window(qkv, out, G, M, H, Hkv, dh, window, sinks=0, lens=None, dtype="bf16", stream=None) -> None:
     """Attention over a sliding window (0: none) and the first `sinks` tokens; lens: int32 [G] on the device or None."""
+    if not isinstance(qkv, int):
+        _same_device(qkv.get_device(), out, lens)
     _check(_lib.rmt_attention_window(_whole(qkv, G * M * (H + 2 * Hkv) * dh, dtype), _whole(out, G * M * H * dh, dtype),
                                      G, M, H, Hkv, dh, window, sinks, _ptr32(lens, G), DTYPES[dtype],
                                      _stream(stream)), "rmt_attention_window")
@@ -420,6 +435,7 @@ class Cache:
         self.ref = ctypes.byref(struct)
         self.n_seqs, self.head_dim = struct.n_seqs, struct.head_dim
         self.width = struct.n_kv_heads * struct.head_dim
+        self.device = keep[0].get_device()
 
 
 def rmt_cache_page_bytes(n_kv_heads: int, head_dim: int) -> int:
@@ -436,12 +452,14 @@ def rmt_cache(pages, page_table, lens, n_kv_heads: int, head_dim: int) -> Cache:
     page = rmt_cache_page_bytes(n_kv_heads, head_dim)
     if size % page or page_table.ndim != 2 or lens.ndim != 1 or lens.shape[0] != page_table.shape[0]:
         raise ValueError(f"pages must hold whole pages of {page} bytes, page_table [n_seqs, max_pages] and lens [n_seqs]")
+    _same_device(pages.get_device(), page_table, lens)
     s = rmt_cache_struct(_ptr(pages), _ptr32(page_table), _ptr32(lens), size // page, page_table.shape[0],
                          page_table.shape[1], n_kv_heads, head_dim)
     return Cache(s, (pages, page_table, lens))
 
 
 def _cache_rows(fn, name, cache, k, v, M, n_new, dtype, stream):
+    _same_device(cache.device, k, v, n_new)
     pk, ld = _rows(k, cache.n_seqs, M, cache.width, dtype)
     if v.dtype is k.dtype and v.shape == k.shape and v.stride() == k.stride():
         pv = v.data_ptr()
@@ -472,6 +490,7 @@ def rmt_attention_cache_workspace(cache: Cache, n_q: int, H: int, window: int = 
 def rmt_attention_cache(cache: Cache, q, out, n_q, H, window, sinks, workspace, dtype="bf16", stream=None) -> None:
     """Attention of the newest n_q tokens of each sequence (q rows [n_seqs, n_q, H * head_dim], a view into
     wider rows allowed) over the cache. workspace: a uint8 tensor of rmt_attention_cache_workspace bytes."""
+    _same_device(cache.device, q, out, workspace)
     pq, ldq = _rows(q, cache.n_seqs, n_q, H * cache.head_dim, dtype)
     _check(_lib.rmt_attention_cache(cache.ref, pq, ldq, _whole(out, cache.n_seqs * n_q * H * cache.head_dim, dtype),
                                     n_q, H, window, sinks,

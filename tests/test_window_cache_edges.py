@@ -138,3 +138,62 @@ def test_sync_names_every_fault_of_the_word(cuda_ok):
     e = sync_error()
     assert e.status == rmt.RMT_ETIMEOUT
     assert "wait gave up" in str(e) and "page table entry" in str(e)
+
+
+# ------------------------------------------------------------------------------------ devices
+
+class On:
+    """A host tensor that says it is on another device (the calls are refused, or reach a fake library)."""
+
+    def __init__(self, t, device):
+        self.t, self.device = t, device
+
+    def get_device(self):
+        return self.device
+
+    def __getattr__(self, name):
+        return getattr(self.t, name)
+
+
+class FakeLibrary:
+    """Notes the calls that reach the library."""
+
+    def __init__(self):
+        self.calls = []
+
+    def __getattr__(self, name):
+        return lambda *a: self.calls.append((name, a)) or 0
+
+
+def streaming_calls(at):
+    """name -> (call, names of its tensors); at(name, tensor) gives the tensor as a call sees it."""
+    i32, bf = torch.int32, torch.bfloat16
+    pages, table, lens = at("pages", torch.zeros(2 * 4608, dtype=torch.uint8)), at("page_table", torch.zeros(2, 1, dtype=i32)), \
+        at("lens", torch.zeros(2, dtype=i32))
+    rows = {n: at(n, torch.zeros(2, 3, 64, dtype=bf)) for n in ("k", "v", "q", "out")}
+    n_new, ws = at("n_new", torch.zeros(2, dtype=i32)), at("workspace", torch.zeros(1 << 16, dtype=torch.uint8))
+    qkv = at("qkv", torch.zeros(2, 3, 192, dtype=bf))
+    cache = lambda: rmt.rmt_cache(pages, table, lens, 1, 64)
+    held = ("pages", "page_table", "lens")
+    return {
+        "write": (lambda: rmt.rmt_cache_write(cache(), rows["k"], rows["v"], 3, n_new=n_new), held + ("k", "v", "n_new")),
+        "read": (lambda: rmt.rmt_cache_read(cache(), rows["k"], rows["v"], 3, n_new=n_new), held + ("k", "v", "n_new")),
+        "attention": (lambda: rmt.rmt_attention_cache(cache(), rows["q"], rows["out"], 3, 1, 0, 0, ws),
+                      held + ("q", "out", "workspace")),
+        "window": (lambda: rmt.rmt_attention_window(qkv, rows["out"], 2, 3, 1, 1, 64, 0, lens=lens), ("qkv", "out", "lens"))}
+
+
+@pytest.mark.parametrize("call", ["write", "read", "attention", "window"])
+def test_tensors_on_another_device_or_the_host_are_refused(monkeypatch, call):
+    fake = FakeLibrary()
+    fake.rmt_cache_page_bytes = rmt.lib().rmt_cache_page_bytes
+    monkeypatch.setattr(rmt, "_lib", fake)
+    run, names = streaming_calls(lambda name, t: On(t, 0))[call]
+    run()
+    assert len(fake.calls) == 1
+    for other in (-1, 1):
+        for bad in names:
+            run, _ = streaming_calls(lambda name, t: On(t, other if name == bad else 0))[call]
+            with pytest.raises(ValueError):
+                run()
+    assert len(fake.calls) == 1
