@@ -221,19 +221,23 @@ _ROW_TYPES = {"torch.bfloat16": "bf16", "torch.float32": "f32"}
 _row_types = {}  # dtype -> its name above, as far as seen
 
 
-_current_stream = None  # () -> the raw current stream, once CUDA was found available
+_current_stream = None  # device index -> its raw current stream, once CUDA was found available
 
 
-def _stream(stream):
+def _stream(stream, device=None):
+    """Raw stream; None: the current one of `device` (None: of the current device)."""
     if stream is None:
         global _current_stream
         if _current_stream is None:
             import torch
             if not torch.cuda.is_available():
                 return None
-            raw, device = getattr(torch._C, "_cuda_getCurrentRawStream", None), torch.cuda.current_device
-            _current_stream = (lambda: raw(device())) if raw else (lambda: torch.cuda.current_stream().cuda_stream)
-        return _current_stream()
+            _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+                lambda d: torch.cuda.current_stream(d).cuda_stream)
+        if device is None or device < 0:
+            import torch
+            device = torch.cuda.current_device()
+        return _current_stream(device)
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
@@ -419,11 +423,13 @@ def rmt_rmsnorm(x, g, y, rows, d, eps, dtype="f32", stream=None) -> None:
 
 def rmt_attention_window(qkv, out, G, M, H, Hkv, dh, window, sinks=0, lens=None, dtype="bf16", stream=None) -> None:
     """Attention over a sliding window (0: none) and the first `sinks` tokens; lens: int32 [G] on the device or None."""
+    device = None
     if not isinstance(qkv, int):
-        _same_device(qkv.get_device(), out, lens)
+        device = qkv.get_device()
+        _same_device(device, out, lens)
     _check(_lib.rmt_attention_window(_whole(qkv, G * M * (H + 2 * Hkv) * dh, dtype), _whole(out, G * M * H * dh, dtype),
                                      G, M, H, Hkv, dh, window, sinks, _ptr32(lens, G), DTYPES[dtype],
-                                     _stream(stream)), "rmt_attention_window")
+                                     _stream(stream, device)), "rmt_attention_window")
 
 
 class Cache:
@@ -467,7 +473,8 @@ def _cache_rows(fn, name, cache, k, v, M, n_new, dtype, stream):
         pv, ldv = _rows(v, cache.n_seqs, M, cache.width, dtype)
         if ld != ldv:
             raise ValueError("k and v need the same row stride")
-    _check(fn(cache.ref, pk, pv, ld, M, _ptr32(n_new, cache.n_seqs), DTYPES[dtype], _stream(stream)), name)
+    _check(fn(cache.ref, pk, pv, ld, M, _ptr32(n_new, cache.n_seqs), DTYPES[dtype],
+              _stream(stream, cache.device)), name)
 
 
 def rmt_cache_write(cache: Cache, k, v, M, n_new=None, dtype="bf16", stream=None) -> None:
@@ -495,7 +502,7 @@ def rmt_attention_cache(cache: Cache, q, out, n_q, H, window, sinks, workspace, 
     _check(_lib.rmt_attention_cache(cache.ref, pq, ldq, _whole(out, cache.n_seqs * n_q * H * cache.head_dim, dtype),
                                     n_q, H, window, sinks,
                                     _ptr(workspace), workspace.numel() * workspace.element_size(), DTYPES[dtype],
-                                    _stream(stream)), "rmt_attention_cache")
+                                    _stream(stream, cache.device)), "rmt_attention_cache")
 
 
 def storage(a, dtype: str, device=None):

@@ -197,3 +197,15 @@ def test_tensors_on_another_device_or_the_host_are_refused(monkeypatch, call):
             with pytest.raises(ValueError):
                 run()
     assert len(fake.calls) == 1
+
+
+@pytest.mark.parametrize("call", ["write", "read", "attention", "window"])
+@pytest.mark.parametrize("device", [0, 3])
+def test_calls_go_to_the_current_stream_of_their_tensors_device(monkeypatch, call, device):
+    fake = FakeLibrary()
+    fake.rmt_cache_page_bytes = rmt.lib().rmt_cache_page_bytes
+    monkeypatch.setattr(rmt, "_lib", fake)
+    monkeypatch.setattr(rmt, "_current_stream", lambda d: 7000 + d)
+    streaming_calls(lambda name, t: On(t, device))[call][0]()
+    (name, args), = fake.calls
+    assert args[-1] == 7000 + device
