@@ -349,6 +349,14 @@ def rmt_get_trace(h: Handle, n_cells: int) -> np.ndarray:
 
 
 def rmt_sync(h: Handle | None, stream=None) -> None:
+    """Wait for `stream` and raise what the device met (without a handle: the kernel-level entry points on the
+    stream's device; a default stream's handle is 0 on every device, so that device is made the current one)."""
+    device = getattr(stream, "device", None)
+    if h is None and device is not None:
+        import torch
+        with torch.cuda.device(device):
+            _check(_lib.rmt_sync(None, stream.cuda_stream), "rmt_sync")
+        return
     _check(_lib.rmt_sync(h.ptr if h is not None else None, _stream(stream)), "rmt_sync")
 
 

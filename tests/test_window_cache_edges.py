@@ -129,6 +129,8 @@ def test_sync_reports_what_a_device_met_that_is_not_the_current_one(cuda_ok):
         met_bad_page("cuda:1", stream)
         rmt.rmt_sync(None)  # device 0 met nothing
         assert sync_error(stream).status == rmt.RMT_EINVAL
+        met_bad_page("cuda:1", torch.cuda.default_stream(1))
+        assert sync_error(torch.cuda.default_stream(1)).status == rmt.RMT_EINVAL
 
 
 @gpu
@@ -209,3 +211,28 @@ def test_calls_go_to_the_current_stream_of_their_tensors_device(monkeypatch, cal
     streaming_calls(lambda name, t: On(t, device))[call][0]()
     (name, args), = fake.calls
     assert args[-1] == 7000 + device
+
+
+def test_sync_on_another_devices_default_stream_makes_that_device_current(monkeypatch):
+    seen = []
+
+    class Current:
+        def __init__(self, device):
+            self.device = device
+
+        def __enter__(self):
+            seen.append(("enter", self.device))
+
+        def __exit__(self, *a):
+            seen.append(("exit", self.device))
+
+    class Library:
+        def rmt_sync(self, h, stream):
+            seen.append((h, stream))
+            return 0
+
+    monkeypatch.setattr(torch.cuda, "device", Current)
+    monkeypatch.setattr(rmt, "_lib", Library())
+    stream = type("Stream", (), dict(device=torch.device("cuda", 3), cuda_stream=0))()
+    rmt.rmt_sync(None, stream=stream)
+    assert seen == [("enter", stream.device), (None, 0), ("exit", stream.device)]
