@@ -431,7 +431,10 @@ __global__ void __launch_bounds__(32 * Shape<DH, T, NT>::WARPS, 1) cache_attn_ke
           if constexpr (SPLIT) q[j][1][2 * w + (i >> 1)][i & 1] = pack2<__half>(lo_term<__half>(v0), lo_term<__half>(v1));
         }
       fin |= first_pos + tok < 0;  // a row that sees nothing gives zeros whatever it holds
-      const float scale = fin ? down * (kCodeScale * rsqrtf(static_cast<float>(DH)) * 1.4426950408889634f) : NAN;
+      // At most 2^96: a score before it is a multiple of 2^-48 (f16 subnormals both) below 2^28, so it stays in range,
+      // and two scores that differ do so by 2^48, as one with all the weight and one with none.
+      const float scale =
+          fin ? fminf(down * (kCodeScale * rsqrtf(static_cast<float>(DH)) * 1.4426950408889634f), 7.9228163e28f) : NAN;
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         rs[j][c] = __shfl_sync(0xffffffffu, scale, 4 * (2 * t + c));

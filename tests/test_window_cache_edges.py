@@ -236,3 +236,27 @@ def test_sync_on_another_devices_default_stream_makes_that_device_current(monkey
     stream = type("Stream", (), dict(device=torch.device("cuda", 3), cuda_stream=0))()
     rmt.rmt_sync(None, stream=stream)
     assert seen == [("enter", stream.device), (None, 0), ("exit", stream.device)]
+
+
+# ------------------------------------------------------------------------------- extreme queries
+
+@gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("dh,T,n_q", [(64, 300, 1), (64, 5000, 1), (64, 5000, 5), (128, 300, 3), (128, 4000, 1), (32, 5000, 2)])
+def test_cache_attention_of_queries_whose_scores_pass_fp32(cuda_ok, dtype, dh, T, n_q):
+    """Queries near the type's end: scores up to 10^41, of either sign. All the weight is one key's, or equal keys'."""
+    H, Hkv = 6, 2
+    s = Setup([T], Hkv, dh)
+    k = torch.full((1, T, Hkv, dh), 4.0, device="cuda")
+    k[:, T // 3] = 7.0  # the largest score of positive queries
+    k[:, T // 2] = 0.25  # the least negative of negative ones
+    k[:, :, 1] *= torch.linspace(0.5, 2.0, T, device="cuda")[None, :, None]
+    v = normal(5, (1, T, Hkv * dh), "f32")
+    rmt.rmt_cache_write(s.cache, k.reshape(1, T, -1), v, T, dtype="f32")
+    gain = torch.tensor([3e38, -3e38, 2e36, -3e38, 3e38, -1e37], device="cuda")
+    q = gain[None, None, :, None].expand(1, n_q, H, dh).to(TORCH[dtype]).reshape(1, n_q, -1).contiguous()
+    got = f64(s.attend(q, n_q, H, 0, 0, dtype))
+    rmt.rmt_sync(None)
+    (kk, vv), = s.values()
+    ref = attend_ref(f64(q)[0].reshape(n_q, H, dh), kk, vv, np.arange(T - n_q, T), 0, 0)
+    check_attention(got[0].reshape(n_q, H, dh), ref, np.abs(vv).max(), dtype)
