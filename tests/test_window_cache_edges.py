@@ -260,3 +260,164 @@ def test_cache_attention_of_queries_whose_scores_pass_fp32(cuda_ok, dtype, dh, T
     (kk, vv), = s.values()
     ref = attend_ref(f64(q)[0].reshape(n_q, H, dh), kk, vv, np.arange(T - n_q, T), 0, 0)
     check_attention(got[0].reshape(n_q, H, dh), ref, np.abs(vv).max(), dtype)
+
+
+# --------------------------------------------------- bounds that one term of 16 bits does not meet
+
+def attend_and_bound(q, k, v, i, window, sinks, score, key, total, floor=0.0):
+    """The formula in 64 bits and how far a result may be off it, for rows of every head of one sequence.
+
+    A score s_j = sum_c q_c k_jc / sqrt(dh) that is off by `score` of a_j = sum_c |q_c k_jc| / sqrt(dh), and a weight that
+    is off by `key` of itself, move the result by at most sum_j p_j |v_j - out| (score a_j + key) to first order (1%
+    on top for the rest). Sums of weights and of weighted values, each off by `total` of the sum of its terms'
+    magnitudes, add 2 total sum_j p_j |v_j|. Weights that are also off by `floor` of the largest one, however small they
+    are themselves, add floor sum_j |v_j - out|: the largest is at most 1 of their sum."""
+    rows, H, dh = q.shape
+    Hkv = k.shape[1]
+    seen = visible(i, np.arange(k.shape[0]), window, sinks)
+    out, tol = np.zeros(q.shape), np.zeros(q.shape)
+    for h in range(H):
+        kh, vh = k[:, h // (H // Hkv)], v[:, h // (H // Hkv)]
+        for r in range(rows):
+            at = np.nonzero(seen[r])[0]
+            if at.size == 0:
+                continue
+            s, a = kh[at] @ q[r, h] / np.sqrt(dh), np.abs(kh[at]) @ np.abs(q[r, h]) / np.sqrt(dh)
+            p = np.exp(s - s.max())
+            p /= p.sum()
+            out[r, h] = o = p @ vh[at]
+            tol[r, h] = 1.01 * ((p * (score * a + key)) @ np.abs(vh[at] - o)) + 2 * total * (p @ np.abs(vh[at])) + \
+                floor * np.abs(vh[at] - o).sum(0)
+    return out, tol
+
+
+def cache_bounds(dh, dtype, units, items):
+    """score, key and total above for the cache kernel, and the result's own rounding.
+
+    Operands: fp32 queries and weights as two f16 terms (2^-22 of a value). f16's smallest step is 2^-24: a weight's last term
+    rounds by up to 2^-25 while the largest is held at 2^7 or more, so every weight, down to those that become 0, is off by
+    up to 2^-32 of the largest (`floor`); a query's by 2^-35 of the row's largest, in the 4 of `score`. A tensor
+    core's step sums 16 products; a step is taken to lose 2^-22 of its terms' magnitudes. dh / 16 steps a
+    score (twice with two terms), 4 a unit of 64 keys, the units of a warp after one another, the parts of an item after those.
+    The exponential is off by 2^-22, its argument's two roundings by 2^-23 of the scores' size, in `score`
+    since a_j >= |s_j|, twice for a reference that was raised. bf16: weights are f16 (2^-11 of a value), and their sum
+    takes them as rounded; the result is bf16 (2^-8)."""
+    f32 = dtype == "f32"
+    terms = 2 if f32 else 1
+    steps = terms * 4 * -(-units * items // (8 * 148)) + units
+    return dict(score=(terms * dh / 16 + f32 + 4) * 2.0 ** -22, key=2.0 ** -22 + (2.0 ** -22 if f32 else 2.0 ** -11),
+                total=steps * 2.0 ** -22, floor=2.0 ** -32), 2.0 ** -24 if f32 else 2.0 ** -8
+
+
+def window_bounds(dh, n):
+    """The same for the fp32 window kernel, n the most keys a row sees: dh FMA a score, the query's scale two roundings,
+    the difference from the maximum one of at most twice a_j; exp2 two units of its last place; n terms a sum, in tiles
+    whose maxima change the earlier ones by another such weight and product (one tile in 64 keys, and one for the sinks)."""
+    u = 2.0 ** -24
+    return dict(score=(dh + 2 + 2 + 1) * u, key=4 * u, total=(n + 6 * (n // 64 + 2)) * u), u
+
+
+def check_bounds(got, ref, tol, rounding):
+    err = np.abs(got - ref)
+    ok = err <= tol + rounding * np.abs(ref)
+    assert np.isfinite(got).all() and ok.all(), (float(err.max()), float((err / np.maximum(tol, 1e-300)).max()))
+
+
+@gpu
+@pytest.mark.parametrize("dh,T", [(64, 40), (64, 9), (128, 40), (32, 50), (64, 130)])
+def test_fp32_cache_attention_carries_more_than_one_f16_term(cuda_ok, dh, T):
+    H, Hkv, n_q = 16, 4, 4
+    s = Setup([T], Hkv, dh)
+    s.fill(81)
+    q = normal(82, (1, n_q, H * dh), "f32") * 2
+    got = f64(s.attend(q, n_q, H, 0, 0, "f32"))
+    rmt.rmt_sync(None)
+    (k, v), = s.values()
+    units = -(-T // (32 if dh == 128 else 64))
+    bounds, rounding = cache_bounds(dh, "f32", units, 8)
+    ref, tol = attend_and_bound(f64(q)[0].reshape(n_q, H, dh), k, v, np.arange(T - n_q, T), 0, 0, **bounds)
+    check_bounds(got[0].reshape(n_q, H, dh), ref, tol, rounding)
+
+
+@gpu
+@pytest.mark.parametrize("dh,M,window,sinks", [(64, 200, 60, 3), (128, 150, 0, 0), (32, 300, 64, 64), (64, 130, 1, 2)])
+def test_fp32_window_attention_carries_fp32(cuda_ok, dh, M, window, sinks):
+    H, Hkv = 6, 2
+    qkv = normal(83, (2, M, (H + 2 * Hkv) * dh), "f32")
+    out = torch.zeros(2, M, H * dh, device="cuda")
+    rmt.rmt_attention_window(qkv, out, 2, M, H, Hkv, dh, window, sinks, dtype="f32")
+    rmt.rmt_sync(None)
+    bounds, rounding = window_bounds(dh, min(M, window + sinks) if window else M)
+    for g in range(2):
+        q, k, v = (t.reshape(M, -1, dh) for t in np.split(f64(qkv)[g], [H * dh, (H + Hkv) * dh], axis=1))
+        ref, tol = attend_and_bound(q, k, v, np.arange(M), window, sinks, **bounds)
+        check_bounds(f64(out)[g].reshape(M, H, dh), ref, tol, 3 * rounding)
+
+
+# --------------------------------------------------------------- the list of units that all share
+
+SHARED = [  # dh, H, Hkv, lens, n_q, window, sinks, max_pages: more than 32 units an item can have
+    (64, 8, 2, [5000, 300, 0, 2100], 1, 0, 0, None), (64, 32, 8, [5000, 4097, 64], 1, 3001, 70, None),
+    (64, 12, 2, [5000, 0, 33], 2, 2999, 70, None), (64, 8, 2, [4200, 5000], 3, 0, 0, None),
+    (64, 16, 2, [4800], 5, 3000, 1, None), (64, 6, 1, [2500, 1, 3000], 64, 2100, 130, None),
+    (32, 8, 2, [5000, 70], 1, 3001, 70, None), (32, 8, 2, [5000], 4, 0, 0, None), (32, 8, 1, [0, 4000, 3], 5, 2200, 64, None),
+    (128, 8, 2, [3000, 129, 0], 1, 1500, 70, None), (128, 4, 1, [2500, 1400], 3, 1301, 33, None),
+    (128, 16, 2, [2200], 5, 0, 0, None), (64, 8, 8, [100, 0, 1, 64, 65], 1, 0, 0, 400), (128, 8, 2, [40, 257], 2, 0, 0, 300),
+    (64, 8, 2, [5000, 5000, 5000, 5000, 5000] * 8, 1, 4000, 4, None)]
+
+
+@gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("dh,H,Hkv,lens,n_q,window,sinks,max_pages", SHARED)
+def test_cache_attention_of_long_items_equals_the_formula(cuda_ok, dtype, dh, H, Hkv, lens, n_q, window, sinks, max_pages):
+    s = Setup(lens, Hkv, dh, seed=len(lens), max_pages=max_pages)
+    s.fill(91)
+    n, rows = len(lens), n_q * (H // Hkv)
+    q = normal(92, (n, n_q, H * dh), dtype) * 2
+    got = f64(s.attend(q, n_q, H, window, sinks, dtype))
+    rmt.rmt_sync(None)
+    tok = 32 if dh == 128 else 64
+    units = max(lens) // tok + 1
+    tiles = -(-rows // (16 if dtype == "bf16" and rows > 8 else 8))
+    held = s.values()
+    for b in range(0, n, max(1, n // 5)):
+        k, v = held[b]
+        pos = np.arange(lens[b] - n_q, lens[b])
+        bounds, rounding = cache_bounds(dh, dtype, units, n * Hkv * tiles)
+        ref, tol = attend_and_bound(f64(q)[b].reshape(n_q, H, dh), k, v, pos, window, sinks, **bounds)
+        check_bounds(got[b].reshape(n_q, H, dh), ref, tol, rounding)
+        assert not got[b].reshape(n_q, -1)[pos < 0].any()
+
+
+@gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("dh,group,T,n_q,window,sinks", [
+    (64, 1, 900, 2, 300, 70), (64, 4, 5000, 2, 3001, 70), (64, 4, 5000, 3, 2900, 64), (128, 2, 700, 1, 301, 33),
+    (128, 4, 3000, 3, 1700, 31), (32, 4, 5000, 5, 2950, 129), (32, 1, 600, 1, 70, 1)])
+def test_each_visible_token_and_no_other_decides(cuda_ok, dtype, dh, group, T, n_q, window, sinks):
+    """A key/value head for each token at a border, whose key outweighs all others where it is visible."""
+    lo = T - n_q - window + 1  # the first row's oldest key
+    at = [0, sinks - 1, sinks, lo - 1, lo, lo + n_q - 1, lo + 64 - lo % 64, T - n_q, T - 1, T - 2]
+    Hkv = len(at)
+    H = group * Hkv
+    s = Setup([T], Hkv, dh)
+    sign = torch.sign(normal(93, (Hkv, dh), "f32"))
+    k = normal(94, (1, T, Hkv, dh), "f32") * 0.3
+    for h, t in enumerate(at):
+        k[0, t, h] = 4 * sign[h]
+    v = normal(95, (1, T, Hkv * dh), "f32")
+    rmt.rmt_cache_write(s.cache, k.reshape(1, T, -1), v, T, dtype="f32")
+    q = (12.0 / dh ** 0.5 * sign).repeat_interleave(group, 0)[None, None].expand(1, n_q, H, dh)
+    q = q.to(TORCH[dtype]).reshape(1, n_q, -1).contiguous()
+    got = f64(s.attend(q, n_q, H, window, sinks, dtype))[0].reshape(n_q, H, dh)
+    rmt.rmt_sync(None)
+    (kk, vv), = s.values()
+    pos = np.arange(T - n_q, T)
+    tiles = -(-n_q * group // (16 if dtype == "bf16" and n_q * group > 8 else 8))
+    bounds, rounding = cache_bounds(dh, dtype, T // (32 if dh == 128 else 64) + 1, Hkv * tiles)
+    ref, tol = attend_and_bound(f64(q)[0].reshape(n_q, H, dh), kk, vv, pos, window, sinks, **bounds)
+    check_bounds(got, ref, tol, rounding)
+    seen = visible(pos, np.array(at), window, sinks)
+    for h in range(H):
+        near = np.abs(got[:, h] - vv[at[h // group], h // group]).max(-1) < 0.05
+        np.testing.assert_array_equal(near, seen[:, h // group])
