@@ -467,12 +467,22 @@ __global__ void __launch_bounds__(32 * Shape<DH, T, NT>::WARPS, 1) cache_attn_ke
         const unsigned char* const kc = ring + st * U::BYTES;
         if (!sm100::mbar_wait(bars + 8 * st, ph_out, abort_flag)) dead = true;
         // mask: units that hold keys after some row's position, or before some row's window
-        // rows of the unit: those from `behind` on hold no token, those from `unseen` up to `before` one that no row of
-        // the call sees (after the sinks, before the first row's window). Neither need ever have been written.
-        const int behind = len - key0, before = first_pos - a.span.window + 1 - key0, unseen = a.span.sinks - key0;
-        auto out_of_sight = [&](int r) { return gone || r >= behind || (r < before && r >= unseen); };
         const bool edge = gone || key0 + U::TOK - 1 > first_pos ||
                           (len - 1 - key0 >= a.span.window && key0 + U::TOK > a.span.sinks);
+        if (edge) {
+          // Tokens behind the sequence's end, and those that no row of the call sees (after the sinks, before the first
+          // row's window), need never have been written, and 0 * NaN would reach every row: their scales become 0.
+          const int behind = len - key0, before = first_pos - a.span.window + 1 - key0, unseen = a.span.sinks - key0;
+#pragma unroll
+          for (int r = lane; r < U::TOK; r += 32)
+            if (gone || r >= behind || (r < before && r >= unseen)) {
+              using Row = std::conditional_t<DH == 128, uint2, std::conditional_t<DH == 64, uint32_t, unsigned short>>;
+#pragma unroll
+              for (int v = 0; v < 2; ++v) reinterpret_cast<Row*>(ring + st * U::BYTES + v * U::V_OFF + U::CODES)[r] = Row{};
+            }
+          sm100::fence_proxy_async_smem();  // the stage's next copy comes after these stores
+          __syncwarp();
+        }
         // S^T: keys g and g + 8 of each tile sit at rows (g >> 1) + 4 (g & 1) and 8 further
         const int rk = (g >> 1) + 4 * (g & 1);
         float s[MT][NT][4];
@@ -491,7 +501,6 @@ __global__ void __launch_bounds__(32 * Shape<DH, T, NT>::WARPS, 1) cache_attn_ke
               sb[h] = *reinterpret_cast<const unsigned short*>(sp + 2 * t);
             else
               sb[h] = sp[DH == 64 ? t : t >> 1];
-            if (edge && out_of_sight(r)) sb[h] = 0;  // bytes of any kind
           }
           if (!WIDE) top_scale = max(top_scale, DH == 128 ? max(max(sb[0] & 255u, sb[1] & 255u), max(sb[0], sb[1]) >> 8)
                                                           : max(sb[0], sb[1]));
@@ -611,7 +620,6 @@ __global__ void __launch_bounds__(32 * Shape<DH, T, NT>::WARPS, 1) cache_attn_ke
             else
               lds_words<WV>(vc + r * (DH / 2) + g * (DH / 16), w[k]);
             sb[k] = vc[U::CODES + r * (DH / 16) + (DH == 128 ? g : DH == 64 ? g >> 1 : g >> 2)];
-            if (edge && out_of_sight(r)) sb[k] = 0;  // bytes of any kind: 0 * NaN would reach every row
           }
           const Scale sa = scale_pair<WIDE>((sb[0] + sb[1] * 0x10000u) * 128u),
                       sz = scale_pair<WIDE>((sb[2] + sb[3] * 0x10000u) * 128u);
