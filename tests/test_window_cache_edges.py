@@ -421,3 +421,53 @@ def test_each_visible_token_and_no_other_decides(cuda_ok, dtype, dh, group, T, n
     for h in range(H):
         near = np.abs(got[:, h] - vv[at[h // group], h // group]).max(-1) < 0.05
         np.testing.assert_array_equal(near, seen[:, h // group])
+
+
+# ------------------------------------------------------------------------ graphs and the debug build
+
+@gpu
+def test_two_captured_graphs_that_share_a_workspace(cuda_ok):
+    """Long items (two kernels and the workspace) captured twice with other queries; replayed in turn after the lengths
+    grow, each gives what an eager call gives."""
+    dh, H, Hkv, lens = 64, 8, 2, [4500, 0, 700]
+    s = Setup([t + 8 for t in lens], Hkv, dh, max_pages=80)
+    s.fill(3, "bf16")
+    s.lens.copy_(torch.tensor(lens, dtype=torch.int32))
+    qs = [normal(i, (3, 2, H * dh), "bf16") for i in (1, 2)]
+    outs = [torch.zeros_like(q) for q in qs]
+    ws = torch.empty(rmt.rmt_attention_cache_workspace(s.cache, 2, H, 0, 0), dtype=torch.uint8, device="cuda")
+    run = lambda q, o: rmt.rmt_attention_cache(s.cache, q, o, 2, H, 0, 0, ws)
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        run(qs[0], outs[0])
+    torch.cuda.synchronize()
+    graphs = []
+    for q, o in zip(qs, outs):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            run(q, o)
+    for step in range(3):
+        s.lens.add_(torch.tensor([1, step, 2], dtype=torch.int32, device="cuda"))
+        for g in (graphs[0], graphs[1], graphs[0]):
+            g.replay()
+        got = [o.clone() for o in outs]
+        for q, o, x in zip(qs, outs, got):
+            run(q, o)
+            rmt.rmt_sync(None)
+            assert torch.equal(o, x) and torch.isfinite(x).all() and x[0].any()
+
+
+@gpu
+def test_streaming_operators_of_the_debug_build(cuda_ok):
+    """The library compiled with -DRMT_DEBUG, in a child process, over cases of every kernel."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    assert os.path.exists(rmt.DEBUG_LIB_PATH)
+    cases = ["test_write_and_read_equal_the_formula", "test_cache_attention_equals_the_formula",
+             "test_window_attention_equals_the_formula", "test_many_sequences"]
+    r = subprocess.run([sys.executable, "-m", "pytest", "-q", "-x", "-m", "gpu", "-p", "no:cacheprovider",
+                        *[f"tests/test_window_cache.py::{c}" for c in cases]], cwd=root, capture_output=True, text=True,
+                       timeout=600, env=dict(os.environ, RMT_LIBRARY=rmt.DEBUG_LIB_PATH))
+    assert r.returncode == 0, r.stdout[-4000:] + r.stderr[-2000:]
