@@ -26,7 +26,7 @@ struct OnDeviceOf {
   rmt_status st = RMT_OK;
   explicit OnDeviceOf(const void* p) {
     cudaPointerAttributes attr;
-    const cudaError_t e = cudaPointerGetAttributes(&attr, p);
+    cudaError_t e = cudaPointerGetAttributes(&attr, p);
     if (e != cudaSuccess) {
       cudaGetLastError();
       st = fail(RMT_ECUDA, std::string("cudaPointerGetAttributes: ") + cudaGetErrorString(e));
@@ -37,9 +37,12 @@ struct OnDeviceOf {
       return;
     }
     int cur = -1;
-    if (cudaGetDevice(&cur) == cudaSuccess && cur != attr.device) {
-      if (cudaSetDevice(attr.device) == cudaSuccess) prev = cur;
+    e = cudaGetDevice(&cur);
+    if (e == cudaSuccess && attr.device >= 0 && cur != attr.device) {
+      e = cudaSetDevice(attr.device);
+      if (e == cudaSuccess) prev = cur;
     }
+    if (e != cudaSuccess) st = fail(RMT_ECUDA, std::string("the tensors' device: ") + cudaGetErrorString(e));
   }
   ~OnDeviceOf() {
     if (prev >= 0) cudaSetDevice(prev);
