@@ -438,6 +438,7 @@ def test_two_captured_graphs_that_share_a_workspace(cuda_ok):
     ws = torch.empty(rmt.rmt_attention_cache_workspace(s.cache, 2, H, 0, 0), dtype=torch.uint8, device="cuda")
     run = lambda q, o: rmt.rmt_attention_cache(s.cache, q, o, 2, H, 0, 0, ws)
     side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
     with torch.cuda.stream(side):
         run(qs[0], outs[0])
     torch.cuda.synchronize()
@@ -471,3 +472,21 @@ def test_streaming_operators_of_the_debug_build(cuda_ok):
                         *[f"tests/test_window_cache.py::{c}" for c in cases]], cwd=root, capture_output=True, text=True,
                        timeout=600, env=dict(os.environ, RMT_LIBRARY=rmt.DEBUG_LIB_PATH))
     assert r.returncode == 0, r.stdout[-4000:] + r.stderr[-2000:]
+
+
+@gpu
+@pytest.mark.parametrize("dh,group,n,longest", [(64, 2, 1200, 2048), (64, 5, 2500, 2047), (128, 4, 1300, 1024), (32, 1, 3000, 1000)])
+def test_more_short_items_than_warps_can_share(cuda_ok, dh, group, n, longest):
+    """Whole items that one or two warps of a CTA take alone, of up to 32 units, several after one another."""
+    lens = [(i * 37) % 90 if i % 40 else longest - i // 40 for i in range(n)]
+    s = Setup(lens, 1, dh)
+    s.fill(3, "bf16")
+    q = normal(4, (n, 1, group * dh), "bf16")
+    got = f64(s.attend(q, 1, group, 0, 0, "bf16"))
+    rmt.rmt_sync(None)
+    held = s.values()
+    bounds, rounding = cache_bounds(dh, "bf16", 32, 8 * 148)  # a warp may have all 32 units of an item
+    for b in list(range(0, n, 200)) + list(range(7, n, 97)) + [n - 1]:
+        k, v = held[b]
+        ref, tol = attend_and_bound(f64(q[b]).reshape(1, group, dh), k, v, np.array([lens[b] - 1]), 0, 0, **bounds)
+        check_bounds(got[b].reshape(1, group, dh), ref, tol, rounding)
