@@ -391,6 +391,10 @@ rmt_status rmt_rmsnorm(const float* x, const void* g, void* y, int32_t rows, int
  * values, and their out rows are left as they were. What a row does not see cannot reach it,
  * even if it is not finite; a row that sees a value that is not finite gets an out row of that
  * head that is not finite (which of inf and NaN, and in which channels, is not specified).
+ * Statistics and sums are fp32; in bf16 the weights are rounded to bf16 before they meet the values.
+ * A row's scores, and its values added up before the division by the weights' sum (the largest
+ * value times 2^12, or times the keys it sees), have to stay within fp32's range. out must not
+ * overlap qkv.
  * Pointers 16-byte aligned; G, H <= 65535, M <= 2^30. */
 rmt_status rmt_attention_window(const void* qkv, void* out, int32_t G, int32_t M, int32_t H, int32_t Hkv,
                                 int32_t dh, int32_t window, int32_t sinks, const int32_t* lens, rmt_dtype dtype,
@@ -445,11 +449,15 @@ size_t rmt_attention_cache_workspace(const rmt_cache* c, int32_t n_q, int32_t H,
  * lens[b] - 1, each seeing what it may of the cache, the newest tokens included, so write them
  * first) over the pages. q: row i of sequence b starts at element (b*n_q + i)*ldq and holds H*head_dim
  * values; out [n_seqs, n_q, H*head_dim]; both in dtype (RMT_F32 or RMT_BF16). Keys and values are
- * the ones rmt_cache_read gives; softmax and sums in fp32. A row that sees no key (a
+ * the ones rmt_cache_read gives. Softmax statistics and all sums are fp32; the products take fp32
+ * queries and weights as two f16 terms (22 bits), bf16 queries as they are and their weights as
+ * one (11 bits); weights below 2^-32 of a row's largest may count as 0. A row that sees no key (a
  * negative position) gives zeros. A token that no row of the call sees need never have been
- * written, and a page without any other is not looked up. The workspace needs no initial value and may be used again by
- * later calls on the same stream; calls that may overlap (two streams, two graphs replayed at
- * once) need one each. Equal calls give equal bits. */
+ * written, and a page without any other is not looked up. The workspace needs no initial value and
+ * may be used again by later calls on the same stream; calls that may overlap (two streams, two
+ * graphs replayed at once) need one each. Equal calls give equal bits; a sequence's may depend on
+ * the lengths of the others, not on their queries, keys or values. lens and the table must not
+ * change while a call runs; out must not overlap q. */
 rmt_status rmt_attention_cache(const rmt_cache* c, const void* q, int64_t ldq, void* out, int32_t n_q, int32_t H,
                                int32_t window, int32_t sinks, void* workspace, size_t workspace_bytes,
                                rmt_dtype dtype, void* stream);

@@ -14,10 +14,13 @@
 //     order of the keys: no atomics, equal bits.
 // Each warp has its own ring of bulk copies.
 //
-// Bound by instructions, not by HBM: 64 sequences of 1 to 8192 tokens (166 MB; 32 / 8 heads of 64, bf16) take
-// 51 us and 5 for the second kernel, 3.0 TB/s, with the schedulers issuing in 54% of all cycles, the integer
-// pipe at 49%, the tensor pipe at 21% and HBM at 41%; one of 131,072 tokens 33 us in all, of which 3 go to
-// the chain of length, page number and codes before the first product.
+// What it takes: 64 sequences of up to 8192 tokens (166 MB; 32 / 8 heads of 64, bf16) 50 us in a run of calls,
+// 3.3 TB/s; alone under the profiler 46.7 us and 8.9 for the second kernel. No unit is full: the schedulers
+// issue in 51% of all cycles, the integer pipe is at 41%, the half2 pipe at 39%, HBM at 45%, the tensor pipe at 23%.
+// Four warps a scheduler do not cover one another's waits, per issued instruction 1.4 for results of fixed
+// latency, 0.9 for a pipe that issues every other cycle, 0.7 for memory. Fewer instructions a code would bring it
+// nearer to HBM. One sequence of 131,072 tokens 31 us in all, of which 3 go to the chain of length, page number and
+// codes before the first product.
 //
 // Arithmetic. Query rows are the MMA's N (8 or 16 rows: the heads of a group, times the tokens),
 // keys or channels its M, so that few rows waste nothing: S^T = K Q^T, O^T = V^T P^T
@@ -31,7 +34,7 @@
 // whole lines of shared memory. P^T turns from accumulator to operand layout by
 // movmatrix. Queries are scaled by a power of two per row into f16's normal range: exact for
 // bf16; fp32 queries and weights are taken as two f16 terms (22 bits). Weights are held at 2^7 to 2^15
-// of their value: what f16 cuts off is below 2^-31 of the largest.
+// of their value; f16's smallest step is 2^-24, so what it cuts off is at most 2^-32 of the largest.
 #include "cache4.cuh"
 #include "launch.h"
 #include "sm100.cuh"
@@ -162,7 +165,7 @@ __device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t b, uint32_t c) {
 // largest scales, 8192 and 9216, whose 1032nd overflows. WIDE takes the low nibble as
 // (1024 + l + 16 h) - 16 (64 + h) first, one operation more, for those.
 // One shift per word: shifts and logic (the ALU pipe) and half2 operations (the heavy half of
-// the FMA pipe) both issue every other cycle, and are what bounds the kernel.
+// the FMA pipe) both issue every other cycle, and are the two fullest (41 and 39%).
 template <bool WIDE>
 __device__ __forceinline__ void dequant(uint32_t w, const Scale& s, uint32_t (&v)[4]) {
 #pragma unroll
@@ -196,9 +199,9 @@ struct Item {
 };
 
 // Warps of a CTA, one CTA per SM: 16 of at most 128 registers, but fewer with more where they would spill too
-// much. 64 sequences of 8192 tokens, bf16: two row tiles of 128 channels (16 heads to one) 8 warps 41 us, 12
-// 48; two of 64 channels (32 heads to two, 16,384 tokens) 12 warps 66, 16 75; fp32 of 128 channels
-// (32 / 8 heads) 12 warps 185, 16 197; one tile of bf16 of 128 channels 16 warps 148, 12 154. (Of
+// much. 64 sequences of 8192 tokens, bf16: two row tiles of 128 channels (16 heads to one) 8 warps 42 us, 12
+// 48; two of 64 channels (32 heads to two, 16,384 tokens) 12 warps 65, 16 71; fp32 of 128 channels
+// (32 / 8 heads) 12 warps 180, 16 193; one tile of bf16 of 128 channels 16 warps 143, 12 152. (Of
 // two CTAs with 8 warps each the first on an SM is served first: it ended after 38 us of 64 sequences'
 // 50, the other's four warps per scheduler then ran alone.)
 template <int DH, typename T, int NT>
@@ -867,10 +870,12 @@ long long most_units(int max_pages, int n_q, int dh, int window, int sinks) {
 }
 // Whether items are dealt whole. Whole, an item takes its warps' share of the longest one's units; dealt in
 // stretches, the average, and a second kernel. bf16, 32 / 8 heads of 64, all lengths alike, whole and in
-// stretches, for 2048, 4096 and 8192 tokens (32, 64 and 128 units): one sequence (8 items) 9.4 and 9.8, 14.3 and
-// 10.0, 23.8 and 11.1 us; 8 sequences 9.8 and 12.5, 14.8 and 16.8, 24.2 and 21.3; 16 sequences 10.5 and 16.4,
-// 15.4 and 21.3, 25.3 and 30.5; 64 sequences 24.8 and 30.1, 44.9 and 49.6, 82.1 and 82.3. Where lengths differ
+// stretches, for 2048, 4096 and 8192 tokens (32, 64 and 128 units): one sequence (8 items) 8.6 and 9.3, 13.0 and
+// 9.9, 22.3 and 12.0 us; 8 sequences 10.4 and 13.8, 15.0 and 18.3, 24.1 and 23.2; 16 sequences 11.7 and 18.3,
+// 16.8 and 23.4, 26.5 and 32.4; 64 sequences 25.8 and 32.3, 44.2 and 49.3, 78.7 and 78.5. Where lengths differ
 // the shares of whole items do too, so beyond 32 units only items that have a CTA each and would fill most SMs.
+// What decides is the table's width, since no launch knows the lengths: 64 sequences of 500 tokens take 11.6 us
+// with a table that ends there and 17.1 with one for 131,072.
 bool deal_whole(long long most, long long items) {
   return most <= 32 || (most <= 64 && items >= 64 && items <= 148);
 }
@@ -888,7 +893,7 @@ Plan plan_of(int n_seqs, int max_pages, int n_q, int tiles, int Hkv, int dh, int
   p.units = p.items * most;
   p.whole = deal_whole(most, p.items);
   // the widest team that leaves every item one at once (148 SMs; 64 sequences of 1024 tokens, 512 items: teams
-  // of 4 15.0 us, of 16 25.0; 32 sequences: 10.0 and 13.3)
+  // of 4 16.0 us, of 16 27.7; 32 sequences: 11.4 and 15.0)
   p.team = cta_warps;
   while (p.team > 1 && (cta_warps % p.team || p.team > most || p.items * p.team > 148LL * cta_warps)) --p.team;
   // a short list over all SMs, one unit a warp (one sequence of 4096 tokens 10.0 us, 11.9 with 16 warps a CTA at

@@ -10,7 +10,8 @@
 // when the value it belongs to is not finite; a weight that is too small for fp32 is its smallest number.
 // Bound by the fp32 FMA pipe and the shared-memory reads that feed it: 16 bytes at a time, 8 of them for
 // 64 FMA. Two sequences of 1040 rows, 32 / 8 heads of 64, window 256, 16 sinks: 166 us, 24 TFLOP/s of
-// what is visible; two of 208 rows with 4 / 2 heads, window 64, too few to fill the SMs: 9.0 us.
+// what is visible; 16 sequences 1181 us, 27 TFLOP/s, a third of the pipe; 16 of bf16 heads of 32 755 us, 21 TFLOP/s;
+// two of 208 rows with 4 / 2 heads, window 64, too few to fill the SMs: 9.0 us.
 // Serves fp32, and bf16 heads of 32 (bf16 heads of 64 and 128: attention_window_tc.cu).
 #include "cache4.cuh"
 #include "launch.h"

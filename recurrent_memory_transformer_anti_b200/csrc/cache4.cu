@@ -11,7 +11,9 @@
 // without a division. Blocks with a NaN, a saturating value or a scale below 2^-14, and fp32, take the
 // general way (encode_value). bf16 rows of 8 heads: 67 MB into 19 MB of codes and scales take 15.8 us
 // (5.4 TB/s), 30 MB into 106 MB 25.4 us (5.4 TB/s). What is left is the chain of three loads (length, page,
-// codes) at the head of each wave of CTAs.
+// codes) at the head of each wave of CTAs. fp32 rows, 134 MB and 19 MB of codes and scales: written in 50 us
+// (3.1 TB/s: every block the general way, and 16 bytes a lane at a stride of 64), read in 39 us (3.9 TB/s: a
+// lane's 32 bytes are two stores at a stride of 32, so that each of a warp's stores fills half sectors).
 #include "cache4.cuh"
 #include "launch.h"
 
