@@ -387,10 +387,11 @@ rmt_status rmt_rmsnorm(const float* x, const void* g, void* y, int32_t rows, int
  *   out[g, i, h] = softmax_j(q[g,i,h] . k[g,j,h/(H/Hkv)] / sqrt(dh)) v[g,j,h/(H/Hkv)], j as above.
  * qkv [G, M, (H + 2*Hkv)*dh] (q heads, then k heads, then v heads), out [G, M, H*dh]; dh in
  * {32, 64, 128}; dtype RMT_F32 or RMT_BF16. lens: device int32 [G], the rows each sequence has
- * (clamped to 0 .. M), or NULL (M each); rows behind a sequence's last are not read as keys or
- * values, and their out rows are left as they were. What a row does not see cannot reach it,
- * even if it is not finite; a row that sees a value that is not finite gets an out row of that
- * head that is not finite (which of inf and NaN, and in which channels, is not specified).
+ * (clamped to 0 .. M; not to change while the call runs), or NULL (M each); rows behind a
+ * sequence's last are not taken as keys or values, and their out rows are left as they were. What a
+ * row does not see cannot reach it, even if it is not finite; a row that sees a value that is not
+ * finite gets an out row of that head that is not finite (which of inf and NaN, and in which
+ * channels, is not specified).
  * Statistics and sums are fp32; in bf16 the weights are rounded to bf16 before they meet the values.
  * A row's scores, and its values added up before the division by the weights' sum (the largest
  * value times 2^12, or times the keys it sees), have to stay within fp32's range. out must not

@@ -118,6 +118,9 @@ def test_sync_reports_on_the_stream_it_is_given(cuda_ok):
     for stream in (torch.cuda.Stream(), torch.cuda.default_stream()):
         met_bad_page(stream=stream)
         assert sync_error(stream).status == rmt.RMT_EINVAL
+    for handle in (0, 1, 2):  # NULL, cudaStreamLegacy, cudaStreamPerThread
+        met_bad_page(stream=handle)
+        assert sync_error(handle).status == rmt.RMT_EINVAL
 
 
 @gpu
